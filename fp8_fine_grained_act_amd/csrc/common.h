@@ -146,6 +146,68 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return u >> 16;
 }
 
+// ---- a linear layer's epilogue -----------------------------------------------
+// C = act(z) + residual, z = product + bias.
+struct Epilogue {
+  const float* bias;     // [n] or null
+  const uint16_t* res;   // bf16 [m, n], row stride ldr, or null
+  int64_t ldr;
+  uint16_t* z;           // bf16 [m, n], row stride ldz, or null: z kept for the backward pass
+  int64_t ldz;
+  int act;               // FP8BS_ACT_*
+};
+
+// SiLU and the tanh form of GELU are both z * sigma(v) with sigma(v) = 1 / (1 +
+// e^-v): v = z for SiLU, v = 2 sqrt(2/pi) (z + 0.044715 z^3) for GELU, since
+// (1 + tanh(v/2)) / 2 = sigma(v).  e^-v is one v_exp_f32 (2^x) of v times
+// -log2(e), the quotient one v_rcp_f32; both are within 1 ulp, and v's own
+// rounding adds |v| * 2^-24, so act is exact to about 1e-6 where it is not
+// tiny, far below the bf16 rounding (2^-8) that follows.  Where 2^x overflows,
+// sigma is 0, its limit.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGeluC0 = 1.5957691216057308f;             // 2 sqrt(2/pi)
+constexpr float kGeluC1 = 1.5957691216057308f * 0.044715f;
+
+__device__ __forceinline__ float sigmoid_of(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e));
+}
+
+// GELU's v saturates sigma (to 0 or 1 in binary32) well inside |z| = 16, so z
+// is clipped there first: z^3 then never overflows.
+__device__ __forceinline__ float gelu_clip(float z) { return __builtin_amdgcn_fmed3f(z, -16.0f, 16.0f); }
+
+__device__ __forceinline__ void act_forward4(int act, float (&z)[4]) {
+  if (act == FP8BS_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = fmaxf(z[i], 0.0f);
+  } else if (act == FP8BS_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = gelu_clip(z[i]);
+      z[i] *= sigmoid_of(c * __builtin_fmaf(kGeluC1, c * c, kGeluC0));
+    }
+  } else if (act == FP8BS_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] *= sigmoid_of(z[i]);
+  }
+}
+
+// act'(z): with p = sigma(v), d/dz (z p) = p + z p (1 - p) v'(z).
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == FP8BS_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (ACT == FP8BS_ACT_GELU_TANH) {
+    const float c = gelu_clip(z), cc = c * c;
+    const float p = sigmoid_of(c * __builtin_fmaf(kGeluC1, cc, kGeluC0));
+    return __builtin_fmaf(c * p * (1.0f - p), __builtin_fmaf(3.0f * kGeluC1, cc, kGeluC0), p);
+  }
+  if (ACT == FP8BS_ACT_SILU) {
+    const float p = sigmoid_of(z);
+    return __builtin_fmaf(z * p, 1.0f - p, p);
+  }
+  return 1.0f;
+}
+
 // ---- streaming (non-temporal) 16-byte loads and stores ----------------------
 // For data touched once per kernel (a dispatch payload written far larger than
 // the caches, expert rows gathered once): the accesses carry the non-temporal

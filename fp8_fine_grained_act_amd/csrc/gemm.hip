@@ -53,6 +53,11 @@ namespace fp8bs {
 
 enum GemmMode : int { kFprop = 0, kDgrad = 1, kWgrad = 2, kGrouped = 3 };
 
+// What a forward or dgrad kernel does beside the plain product: kEpi applies
+// bias, activation and residual before the bf16 rounding (store_row_epi),
+// kRagged walks expert segments of any length (ragged_tile).
+enum GemmVariant : int { kPlain = 0, kEpi = 1, kRagged = 2 };
+
 struct GemmArgs {
   const uint8_t* qa;
   const float* sa;
@@ -77,6 +82,7 @@ struct GemmArgs {
   int tile_sel;              // grouped: 0 every tile, 1 only each expert's first m-tile, 2 the others
   int keep_all;              // grouped from bf16 weights with qw: 1 every expert's codes stored, 0 only
                              // those of experts with several m-tiles (the ones read back)
+  Epilogue epi;              // kEpi
 };
 
 // Expert whose segment holds row m0: the largest e with seg[e] <= m0 (empty
@@ -154,6 +160,47 @@ __device__ inline TileMN tile_coords(const GemmArgs& p, uint32_t b) {
   const uint32_t rows = tiles_m - first < gm ? tiles_m - first : gm;
   const uint32_t n = r / rows;
   return TileMN{first + (r - n * rows), n};
+}
+
+// The tile of `bm` rows with index `tm` when every expert's segment is cut into
+// ceil(length / bm) tiles, experts in order: its expert (-1: none, tm is past
+// the last tile), first row and row count.  The whole wave works on it: 64
+// experts per step, their tile counts summed by a scan.  Offsets are clipped to
+// [0, total_rows] and a segment that runs backwards counts as empty, so no
+// device contents lead to a row outside the buffers.
+struct RaggedTile {
+  int e;
+  int64_t m0, rows;
+};
+__device__ __forceinline__ RaggedTile ragged_tile(const int32_t* __restrict__ seg, int num_experts, int64_t total_rows,
+                                                  int tm, int bm, int lane) {
+  const int cap = (int)total_rows;
+  int done = 0;
+  for (int base = 0; base < num_experts; base += 64) {
+    const int e = base + lane;
+    int s0 = 0, len = 0;
+    if (e < num_experts) {
+      s0 = min(max(seg[e], 0), cap);
+      len = max(0, min(max(seg[e + 1], 0), cap) - s0);
+    }
+    const int tiles = (len + bm - 1) / bm;
+    int incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
+    }
+    const uint64_t hit = __ballot(done + incl > tm);
+    if (hit) {
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      const int i = tm - done - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l));
+      const int left = __builtin_amdgcn_readlane(len, l) - i * bm;
+      if (i < 0 || left <= 0) break;
+      return RaggedTile{base + l, (int64_t)__builtin_amdgcn_readlane(s0, l) + (int64_t)i * bm, min(left, bm)};
+    }
+    done += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return RaggedTile{-1, 0, 0};
 }
 
 constexpr int BK = 128;
@@ -241,6 +288,20 @@ struct GemmCfg {
 // 4096x32768x512, 268 MB of bf16: 130 -> 116 us; the MoE grouped GEMM's 535 MB
 // row capacity 2.24 -> 2.18 ms; an output that fits, such as dgrad's
 // 4096x7168, was 5% slower with it).
+__device__ __forceinline__ void store_pair(uint16_t* dst, const float (&x)[4], const float (&y)[4], int stream_out) {
+  const uint32_t x0 = f32_to_bf16_rne(x[0]) | (f32_to_bf16_rne(x[1]) << 16);
+  const uint32_t x1 = f32_to_bf16_rne(x[2]) | (f32_to_bf16_rne(x[3]) << 16);
+  const uint32_t y0 = f32_to_bf16_rne(y[0]) | (f32_to_bf16_rne(y[1]) << 16);
+  const uint32_t y1 = f32_to_bf16_rne(y[2]) | (f32_to_bf16_rne(y[3]) << 16);
+  const auto s0 = __builtin_amdgcn_permlane16_swap(x0, y0, false, false);
+  const auto s1 = __builtin_amdgcn_permlane16_swap(x1, y1, false, false);
+  const uint4 v = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+  if (stream_out)
+    store_nt(dst, v);
+  else
+    *reinterpret_cast<uint4*>(dst) = v;
+}
+
 template <int TN, int TM>
 __device__ __forceinline__ void store_row_bf16(const GemmArgs& p, const v4f (&acc)[TN][TM], int j, int64_t row,
                                                int64_t col0, int g) {
@@ -273,9 +334,60 @@ __device__ __forceinline__ void store_row_bf16(const GemmArgs& p, const v4f (&ac
   }
 }
 
-template <int MODE, int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+// The same pairs of tiles with the epilogue of a linear layer: z = acc + bias,
+// optionally kept (bf16), then act(z) + residual, rounded once.  z and the
+// residual pass through the same 16-byte pieces as the output: the residual's
+// piece is loaded as it will be stored and swapped back (the swap is its own
+// inverse) to the lanes that hold its accumulators.
+template <int TN, int TM>
+__device__ __forceinline__ void store_row_epi(const GemmArgs& p, const v4f (&acc)[TN][TM], int j, int64_t row,
+                                              int64_t col0, int g) {
+  static_assert(TN % 2 == 0, "pairs of tiles");
+  const Epilogue& ep = p.epi;
+  uint16_t* const crow = reinterpret_cast<uint16_t*>(p.c) + row * p.ldc;
+#pragma unroll
+  for (int i = 0; i < TN; i += 2) {
+    const int64_t col = col0 + 16 * i + 16 * (g & 1) + 8 * (g >> 1);
+    if (col >= p.n) continue;                  // 32 columns at a time: all of a row's lanes agree
+    uint4 rv = make_uint4(0, 0, 0, 0);
+    if (ep.res) rv = *reinterpret_cast<const uint4*>(ep.res + row * ep.ldr + col);
+    float x[4], y[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      x[v] = acc[i][j][v];
+      y[v] = acc[i + 1][j][v];
+    }
+    if (ep.bias) {
+      const float* b = ep.bias + col0 + 16 * i + 4 * g;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        x[v] += b[v];
+        y[v] += b[16 + v];
+      }
+    }
+    if (ep.z) store_pair(ep.z + row * ep.ldz + col, x, y, p.stream_out);
+    act_forward4(ep.act, x);
+    act_forward4(ep.act, y);
+    if (ep.res) {
+      const auto r0 = __builtin_amdgcn_permlane16_swap(rv.x, rv.z, false, false);
+      const auto r1 = __builtin_amdgcn_permlane16_swap(rv.y, rv.w, false, false);
+      x[0] += bf16_lo(r0[0]);
+      x[1] += bf16_hi(r0[0]);
+      x[2] += bf16_lo(r1[0]);
+      x[3] += bf16_hi(r1[0]);
+      y[0] += bf16_lo(r0[1]);
+      y[1] += bf16_hi(r0[1]);
+      y[2] += bf16_lo(r1[1]);
+      y[3] += bf16_hi(r1[1]);
+    }
+    store_pair(crow + col, x, y, p.stream_out);
+  }
+}
+
+template <int MODE, int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int VAR = kPlain>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) __attribute__((amdgpu_waves_per_eu(1, 2)))
 void gemm_kernel(GemmArgs p) {
+  static_assert(VAR == kPlain || MODE == kFprop || MODE == kDgrad, "variants of the bf16-output products");
   using C = GemmCfg<MODE, BM, BN, WAVES_M, WAVES_N, STAGES>;
   constexpr int WM = C::WM, WN = C::WN, TM = C::TM, TN = C::TN;
   constexpr int NW = C::kWaves;
@@ -288,9 +400,12 @@ void gemm_kernel(GemmArgs p) {
   const int l16 = lane & 15, g = lane >> 4;
 
   const TileMN tc = tile_coords(p, blockIdx.x);
-  const int64_t m0 = (int64_t)tc.m * BM, n0 = (int64_t)tc.n * BN;
-  const int64_t M = p.m, N = p.n, K = p.k;
+  const RaggedTile rt = VAR == kRagged ? ragged_tile(p.seg, (int)p.num_experts, p.m, (int)tc.m, BM, lane)
+                                       : RaggedTile{0, (int64_t)tc.m * BM, BM};
+  const int64_t m0 = rt.m0, n0 = (int64_t)tc.n * BN;
+  const int64_t M = VAR == kRagged ? m0 + rt.rows : p.m, N = p.n, K = p.k;
   const int nkb = (int)(K / BK);
+  if (VAR == kRagged && rt.e < 0) return;      // more tiles in the grid than the segments hold
 
   // grouped: a tile at or past the end of the last segment holds no expert's
   // rows (the row capacity can exceed the padded total); the workgroup leaves
@@ -299,6 +414,10 @@ void gemm_kernel(GemmArgs p) {
 
   const uint8_t* qb = p.qb;
   const float* sb = p.sb;
+  if (VAR == kRagged) {
+    qb += (int64_t)rt.e * N * K;
+    sb += (int64_t)rt.e * (N / 128) * nkb;
+  }
   if (MODE == kGrouped) {
     // expert whose segment holds row m0: the largest e with seg[e] <= m0
     int lo = 0, hi = (int)p.num_experts;
@@ -502,6 +621,10 @@ void gemm_kernel(GemmArgs p) {
   for (int j = 0; j < TM; ++j) {
     const int64_t row = m0 + WM * wm + 16 * j + l16;
     if (row >= M) continue;
+    if (VAR == kEpi) {
+      store_row_epi<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
+      continue;
+    }
     if (MODE != kWgrad) {
       store_row_bf16<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       continue;
@@ -563,19 +686,25 @@ static int64_t choose_group_m(const GemmArgs& a, int64_t bm, int64_t bn, int64_t
   return best;
 }
 
-template <int MODE, int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+// Most tiles of bm rows that segments of at most `rows` rows in all can need:
+// every expert that owns a row may leave one tile partly filled.
+static int64_t ragged_tiles(int64_t rows, int64_t num_experts, int64_t bm) {
+  return (rows + (bm - 1) * (num_experts < rows ? num_experts : rows)) / bm;
+}
+
+template <int MODE, int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int VAR = kPlain>
 static int launch_gemm(GemmArgs a, hipStream_t s) {
   a.tiles_n = (a.n + BN - 1) / BN;
-  a.tiles_m = (a.m + BM - 1) / BM;
+  a.tiles_m = VAR == kRagged ? ragged_tiles(a.m, a.num_experts, BM) : (a.m + BM - 1) / BM;
   // grouped GEMM: row-major, so an M tile's rows (one expert's tokens) stay
   // in L2 across its N tiles and the expert's next M tile follows one row of
   // tiles later, while that expert's weight columns are still cached
   // (measured on 256 experts of 4096x7168: 4.09 -> 2.55 ms against the
   // column-major order, which re-reads every expert's rows once per N tile)
-  a.group_m = MODE == kGrouped ? -1 : choose_group_m(a, BM, BN, MODE == kWgrad ? 4 : 2);
+  a.group_m = MODE == kGrouped || VAR == kRagged ? -1 : choose_group_m(a, BM, BN, MODE == kWgrad ? 4 : 2);
   const int64_t grid = a.tiles_m * a.tiles_n;
   if (grid > kMaxGrid) return FP8BS_ERR_SHAPE;
-  hipLaunchKernelGGL((gemm_kernel<MODE, BM, BN, WAVES_M, WAVES_N, STAGES>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((gemm_kernel<MODE, BM, BN, WAVES_M, WAVES_N, STAGES, VAR>), dim3((unsigned)grid),
                      dim3(64 * WAVES_M * WAVES_N), 0, s, a);
   return launch_status();
 }
@@ -1726,4 +1855,41 @@ extern "C" int fp8bs_gemm_wgrad(const uint8_t* qa, const float* sa, const uint8_
   }
   if (use_ws(m, n, true)) return launch_gemm_ws<kWgrad>(a, s, cu_count());
   return launch_gemm<kWgrad, FP8BS_TILE_SMALL>(a, s);
+}
+
+extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb,
+                                   int64_t m, int64_t n, int64_t k, int b_layout, const float* bias, int act,
+                                   const uint16_t* residual, int64_t ldr, uint16_t* z, int64_t ldz, uint16_t* c,
+                                   int64_t ldc, void* stream) {
+  GemmArgs a;
+  const int chk = gemm_check(qa, sa, qb, sb, m, n, k, b_layout, c, ldc, &a);
+  if (chk != FP8BS_OK) return chk;
+  if (act < FP8BS_ACT_NONE || act > FP8BS_ACT_SILU) return FP8BS_ERR_FLAG;
+  if ((residual && ldr < n) || (z && ldz < n)) return FP8BS_ERR_SHAPE;
+  if (!aligned(bias, 4) || (residual && (!aligned(residual, 16) || ldr % 8)) || (z && (!aligned(z, 16) || ldz % 8)))
+    return FP8BS_ERR_ALIGN;
+  a.epi = Epilogue{bias, residual, ldr, z, ldz, act};
+  hipStream_t s = (hipStream_t)stream;
+  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, kEpi>(a, s);
+  return launch_gemm<kDgrad, FP8BS_TILE_SMALL, kEpi>(a, s);
+}
+
+extern "C" int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets,
+                                         int64_t num_experts, int64_t total_rows, const uint8_t* qb, const float* sb,
+                                         int64_t n, int64_t k, int b_layout, uint16_t* c, int64_t ldc, void* stream) {
+  if (!seg_offsets || !qb || !sb || (total_rows > 0 && (!qa || !sa || !c))) return FP8BS_ERR_NULL;
+  if (b_layout != 0 && b_layout != 1) return FP8BS_ERR_FLAG;
+  if (num_experts < 1 || num_experts > 65536 || total_rows < 0 || total_rows > 0x3FFFFFFFLL || n <= 0 || k <= 0 ||
+      n % 128 || k % BK || ldc < n)
+    return FP8BS_ERR_SHAPE;
+  if (!fits_u32(256 * k) || (b_layout == 1 && !fits_u32(k * n))) return FP8BS_ERR_SHAPE;
+  if (!aligned(qa, 16) || !aligned(qb, 16) || !aligned(c, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
+      !aligned(seg_offsets, 4) || ldc % 8)
+    return FP8BS_ERR_ALIGN;
+  if (total_rows == 0) return FP8BS_OK;
+  GemmArgs a{qa, sa, qb, sb, c, ldc, total_rows, n, k, seg_offsets, num_experts, 0, 0, 0, 0, nullptr, 1,
+             total_rows * n * 2 > kStreamBytes};
+  hipStream_t s = (hipStream_t)stream;
+  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, kRagged>(a, s);
+  return launch_gemm<kDgrad, FP8BS_TILE_SMALL, kRagged>(a, s);
 }

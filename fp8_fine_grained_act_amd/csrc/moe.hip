@@ -65,6 +65,7 @@ constexpr int kMaxTopk = 64;               // a token's slots fit in one wave's 
 // serialize in the workgroup's one memory pipeline.
 constexpr int kRouteBatch = 16;
 
+template <int PAD>
 __global__ __launch_bounds__(1024) void moe_route_kernel(const int32_t* __restrict__ ids, int64_t pairs,
                                                          int num_e, int32_t* __restrict__ seg,
                                                          int32_t* __restrict__ slot_rows,
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const int32_t* __restri
       run += c;
     }
     cnt_s[tid] = run;
-    padded = (run + 127) & ~127;
+    padded = (run + PAD - 1) / PAD * PAD;
   }
   int incl = padded;                                   // inclusive scan inside the wave
   for (int d = 1; d < 64; d <<= 1) {
@@ -393,7 +394,25 @@ extern "C" int fp8bs_moe_route(const int32_t* topk_ids, int64_t tokens, int64_t 
   if (!aligned(topk_ids, 4) || !aligned(seg_offsets, 4) || !aligned(slot_rows, 4) || !aligned(row_token, 4))
     return FP8BS_ERR_ALIGN;
   const int64_t pairs = tokens * topk;
-  hipLaunchKernelGGL(moe_route_kernel, dim3(1), dim3(64 * kRouteWaves), 0, (hipStream_t)stream, topk_ids, pairs,
+  hipLaunchKernelGGL(moe_route_kernel<kGroup>, dim3(1), dim3(64 * kRouteWaves), 0, (hipStream_t)stream, topk_ids, pairs,
+                     (int)num_experts, seg_offsets, slot_rows, row_token, rows_cap);
+  if (pairs > 0)
+    hipLaunchKernelGGL(moe_route_rows_kernel, dim3((unsigned)((pairs + 255) / 256)), dim3(256), 0,
+                       (hipStream_t)stream, slot_rows, pairs, (int)topk, row_token, rows_cap);
+  return launch_status();
+}
+
+extern "C" int fp8bs_moe_route_ragged(const int32_t* topk_ids, int64_t tokens, int64_t topk, int64_t num_experts,
+                                      int32_t* seg_offsets, int32_t* slot_rows, int32_t* row_token, int64_t rows_cap,
+                                      void* stream) {
+  if (!seg_offsets || (tokens > 0 && (!topk_ids || !slot_rows)) || (rows_cap > 0 && !row_token))
+    return FP8BS_ERR_NULL;
+  if (!route_sizes_ok(tokens, topk, num_experts) || num_experts > kRouteMaxExperts) return FP8BS_ERR_SHAPE;
+  const int64_t pairs = tokens * topk;
+  if (rows_cap < pairs || rows_cap > 0x7FFFFFFFLL) return FP8BS_ERR_SHAPE;
+  if (!aligned(topk_ids, 4) || !aligned(seg_offsets, 4) || !aligned(slot_rows, 4) || !aligned(row_token, 4))
+    return FP8BS_ERR_ALIGN;
+  hipLaunchKernelGGL(moe_route_kernel<1>, dim3(1), dim3(64 * kRouteWaves), 0, (hipStream_t)stream, topk_ids, pairs,
                      (int)num_experts, seg_offsets, slot_rows, row_token, rows_cap);
   if (pairs > 0)
     hipLaunchKernelGGL(moe_route_rows_kernel, dim3((unsigned)((pairs + 255) / 256)), dim3(256), 0,

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libfp8bs.so")
 
 FP8BS_OK = 0
 GROUP = 128
+FP8BS_ACT_NONE, FP8BS_ACT_RELU, FP8BS_ACT_GELU_TANH, FP8BS_ACT_SILU = 0, 1, 2, 3
 
 _c_void_p, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 
@@ -43,6 +44,15 @@ _SIGNATURES = {
                                    _c_void_p, _i64, _c_void_p, _i64, _c_void_p],
     "fp8bs_moe_combine": [_c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _i64,
                           _c_void_p],
+    "fp8bs_gemm_epilogue": [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _int, _c_void_p, _int,
+                            _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p],
+    "fp8bs_epilogue_backward": [_c_void_p, _i64, _c_void_p, _i64, _i64, _i64, _int, _c_void_p, _i64, _c_void_p, _int,
+                                _c_void_p, _i64, _c_void_p],
+    "fp8bs_moe_route_ragged": [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64, _c_void_p],
+    "fp8bs_grouped_gemm_ragged": [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64, _i64, _int,
+                                  _c_void_p, _i64, _c_void_p],
+    "fp8bs_grouped_wgrad_ragged": [_c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p,
+                                   _int, _c_void_p],
 }
 
 
@@ -66,11 +76,13 @@ def _load():
     lib.fp8bs_status_string.restype = ctypes.c_char_p
     lib.fp8bs_moe_max_rows.argtypes = [_i64, _i64, _i64]
     lib.fp8bs_moe_max_rows.restype = ctypes.c_int64
+    lib.fp8bs_epilogue_backward_workspace.argtypes = [_i64, _i64]
+    lib.fp8bs_epilogue_backward_workspace.restype = ctypes.c_int64
     return lib
 
 
 raw = _load()
-EXPORTED = tuple(_SIGNATURES) + ("fp8bs_status_string", "fp8bs_moe_max_rows")
+EXPORTED = tuple(_SIGNATURES) + ("fp8bs_status_string", "fp8bs_moe_max_rows", "fp8bs_epilogue_backward_workspace")
 
 
 def status_string(status):
@@ -458,3 +470,203 @@ def fp8bs_moe_combine(y, slot_rows, gates, out=None, stream=None):
                                out.data_ptr(), ldo, _stream(stream))
     _check("fp8bs_moe_combine", st)
     return out
+
+
+def _same_device(ref, *named):
+    for t, nm in named:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{nm} must be on {ref.device}")
+
+
+def _on(device, stream):
+    """The stream of the call: the caller's, or the current one of the tensors' device."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream must belong to {device}")
+    return stream
+
+
+def _call(name, device, stream, *args):
+    """Run entry point `name` with the tensors' device current (kernels go to the current device)."""
+    with torch.cuda.device(device):
+        _check(name, getattr(raw, name)(*args, ctypes.c_void_p(stream.cuda_stream)))
+
+
+def _matrix(t, dtype, shape, name):
+    """Checks a [rows, cols] tensor with unit column stride; returns its row stride.
+
+    A tensor of one row has that row's length as its stride whatever torch reports."""
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape) or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be {list(shape)} with unit column stride")
+    return t.stride(0) if shape[0] > 1 else max(shape[1], 8 * -(-shape[1] // 8))
+
+
+def fp8bs_gemm_epilogue(qa, sa, qb, sb, b_layout=0, bias=None, act=FP8BS_ACT_NONE, residual=None, z=None, c=None,
+                        stream=None):
+    """bf16 C [m, n] = act(A B + bias) + residual, operands as for fp8bs_gemm.
+
+    bias f32 [n]; residual bf16 [m, n] (may be c itself); z bf16 [m, n], filled with
+    the pre-activations A B + bias when given (for fp8bs_epilogue_backward)."""
+    _contig(qa, torch.uint8, "qa")
+    _contig(sa, torch.float32, "sa")
+    _contig(qb, torch.uint8, "qb")
+    _contig(sb, torch.float32, "sb")
+    if qa.dim() != 2 or qb.dim() != 2:
+        raise ValueError("qa and qb must be matrices")
+    if b_layout not in (0, 1):
+        raise ValueError("b_layout must be 0 or 1")
+    m, k = qa.shape
+    n, kb = (qb.shape[0], qb.shape[1]) if b_layout == 0 else (qb.shape[1], qb.shape[0])
+    blocks = (qb.shape[0] // GROUP, qb.shape[1] // GROUP)
+    if kb != k or tuple(sa.shape) != (m, k // GROUP) or tuple(sb.shape) != blocks:
+        raise ValueError("operand and scale shapes do not match")
+    if c is None:
+        c = torch.empty((m, n), dtype=torch.bfloat16, device=qa.device)
+    ldc = _matrix(c, torch.bfloat16, (m, n), "c")
+    ldr = _matrix(residual, torch.bfloat16, (m, n), "residual") if residual is not None else 0
+    ldz = _matrix(z, torch.bfloat16, (m, n), "z") if z is not None else 0
+    if bias is not None and tuple(_contig(bias, torch.float32, "bias").shape) != (n,):
+        raise ValueError("bias must be [n]")
+    _same_device(qa, (sa, "sa"), (qb, "qb"), (sb, "sb"), (bias, "bias"), (residual, "residual"), (z, "z"), (c, "c"))
+    _call("fp8bs_gemm_epilogue", qa.device, _on(qa.device, stream), qa.data_ptr(), sa.data_ptr(), qb.data_ptr(),
+          sb.data_ptr(), m, n, k, b_layout, None if bias is None else bias.data_ptr(), int(act),
+          None if residual is None else residual.data_ptr(), ldr, None if z is None else z.data_ptr(), ldz,
+          c.data_ptr(), ldc)
+    return c
+
+
+def fp8bs_epilogue_backward_workspace(m, n):
+    """Bytes of workspace that fp8bs_epilogue_backward needs for dbias (host only)."""
+    r = raw.fp8bs_epilogue_backward_workspace(int(m), int(n))
+    if r < 0:
+        raise Fp8bsError("fp8bs_epilogue_backward_workspace", r)
+    return int(r)
+
+
+def fp8bs_epilogue_backward(dy, z, act=FP8BS_ACT_NONE, dz=None, dbias=None, accumulate=0, workspace=None,
+                            stream=None):
+    """(dz bf16 [m, n], dbias f32 [n]): dz = dy * act'(z), dbias (+)= its column sums.
+
+    z may be None with FP8BS_ACT_NONE.  dz / dbias: a tensor to write (dz may be dy
+    or z), None to allocate one, or False to leave that result out.  workspace: a
+    contiguous float32 tensor of at least fp8bs_epilogue_backward_workspace(m, n)
+    bytes, or None to allocate one."""
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise ValueError("dy must be a bf16 matrix")
+    m, n = dy.shape
+    dev = dy.device
+    ldy = _matrix(dy, torch.bfloat16, (m, n), "dy")
+    ldz = 0
+    if z is not None:
+        ldz = _matrix(z, torch.bfloat16, (m, n), "z")
+    elif act != FP8BS_ACT_NONE:
+        raise ValueError("z is needed for this activation")
+    if accumulate and not isinstance(dbias, torch.Tensor):
+        raise ValueError("accumulate needs a dbias to add to")
+    dz = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if dz is None else (None if dz is False else dz)
+    dbias = torch.empty(n, dtype=torch.float32, device=dev) if dbias is None else (None if dbias is False else dbias)
+    lddz = _matrix(dz, torch.bfloat16, (m, n), "dz") if dz is not None else 0
+    if dbias is not None and tuple(_contig(dbias, torch.float32, "dbias").shape) != (n,):
+        raise ValueError("dbias must be [n]")
+    s = _on(dev, stream)
+    need = fp8bs_epilogue_backward_workspace(m, n) if dbias is not None else 0
+    if workspace is None and need:
+        workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
+        if stream is not None:
+            workspace.record_stream(s)         # kept until that stream has used it
+    if workspace is not None:
+        _contig(workspace, torch.float32, "workspace")
+    _same_device(dy, (z, "z"), (dz, "dz"), (dbias, "dbias"), (workspace, "workspace"))
+    _call("fp8bs_epilogue_backward", dev, s, dy.data_ptr(), ldy, None if z is None else z.data_ptr(), ldz, m, n,
+          int(act), None if dz is None else dz.data_ptr(), lddz, None if dbias is None else dbias.data_ptr(),
+          int(accumulate), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else 4 * workspace.numel())
+    return dz, dbias
+
+
+def fp8bs_moe_route_ragged(topk_ids, num_experts, rows_cap=None, seg_offsets=None, slot_rows=None, row_token=None,
+                           stream=None):
+    """fp8bs_moe_route without padding rows: (seg_offsets [E+1], slot_rows [T, k], row_token [cap]).
+
+    rows_cap (default: tokens * topk) must be at least tokens * topk."""
+    _contig(topk_ids, torch.int32, "topk_ids")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [tokens, topk]")
+    tokens, topk = topk_ids.shape
+    if rows_cap is None:
+        rows_cap = tokens * topk
+    dev = topk_ids.device
+    if seg_offsets is None:
+        seg_offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    if slot_rows is None:
+        slot_rows = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    if row_token is None:
+        row_token = torch.empty(rows_cap, dtype=torch.int32, device=dev)
+    outs = ((seg_offsets, "seg_offsets"), (slot_rows, "slot_rows"), (row_token, "row_token"))
+    for t, nm in outs:
+        _contig(t, torch.int32, nm)
+    if seg_offsets.numel() != num_experts + 1 or tuple(slot_rows.shape) != (tokens, topk) \
+            or row_token.numel() != rows_cap:
+        raise ValueError("output shapes do not match the routing")
+    _same_device(topk_ids, *outs)
+    _call("fp8bs_moe_route_ragged", dev, _on(dev, stream), topk_ids.data_ptr(), tokens, topk, num_experts,
+          seg_offsets.data_ptr(), slot_rows.data_ptr(), row_token.data_ptr(), rows_cap)
+    return seg_offsets, slot_rows, row_token
+
+
+def fp8bs_grouped_gemm_ragged(qa, sa, seg_offsets, qb, sb, b_layout=0, c=None, stream=None):
+    """Expert products over segments of any length: bf16 C [R, n].
+
+    qb [E, n, k] for b_layout 0, [E, k, n] for 1 (the forward weights as stored);
+    seg_offsets int32 [E+1] on the device.  Rows of c outside every segment are left
+    as they are."""
+    _contig(qa, torch.uint8, "qa")
+    _contig(sa, torch.float32, "sa")
+    _contig(qb, torch.uint8, "qb")
+    _contig(sb, torch.float32, "sb")
+    _contig(seg_offsets, torch.int32, "seg_offsets")
+    if qa.dim() != 2 or qb.dim() != 3:
+        raise ValueError("qa must be [rows, k] and qb [experts, ., .]")
+    if b_layout not in (0, 1):
+        raise ValueError("b_layout must be 0 or 1")
+    rows, k = qa.shape
+    num_e = qb.shape[0]
+    n, kb = (qb.shape[1], qb.shape[2]) if b_layout == 0 else (qb.shape[2], qb.shape[1])
+    blocks = (num_e, qb.shape[1] // GROUP, qb.shape[2] // GROUP)
+    if kb != k or tuple(sa.shape) != (rows, k // GROUP) or tuple(sb.shape) != blocks:
+        raise ValueError("operand and scale shapes do not match")
+    if seg_offsets.numel() != num_e + 1:
+        raise ValueError("seg_offsets must have num_experts + 1 entries")
+    if c is None:
+        c = torch.empty((rows, n), dtype=torch.bfloat16, device=qa.device)
+    ldc = _matrix(c, torch.bfloat16, (rows, n), "c")
+    _same_device(qa, (sa, "sa"), (qb, "qb"), (sb, "sb"), (seg_offsets, "seg_offsets"), (c, "c"))
+    _call("fp8bs_grouped_gemm_ragged", qa.device, _on(qa.device, stream), qa.data_ptr(), sa.data_ptr(),
+          seg_offsets.data_ptr(), num_e, rows, qb.data_ptr(), sb.data_ptr(), n, k, b_layout, c.data_ptr(), ldc)
+    return c
+
+
+def fp8bs_grouped_wgrad_ragged(dy, x, seg_offsets, c=None, accumulate=0, stream=None):
+    """Experts' weight gradients f32 C [E, m, n]: C[e] (+)= dy_e^T x_e over the rows of segment e.
+
+    dy bf16 [R, m], x bf16 [R, n]; seg_offsets int32 [E+1] on the device."""
+    if not isinstance(dy, torch.Tensor) or not isinstance(x, torch.Tensor) or dy.dim() != 2 or x.dim() != 2:
+        raise ValueError("dy and x must be bf16 matrices")
+    rows, m = dy.shape
+    n = x.shape[1]
+    ldy = _matrix(dy, torch.bfloat16, (rows, m), "dy")
+    ldx = _matrix(x, torch.bfloat16, (rows, n), "x")
+    _contig(seg_offsets, torch.int32, "seg_offsets")
+    num_e = seg_offsets.numel() - 1
+    if accumulate and c is None:
+        raise ValueError("accumulate needs a c to add to")
+    if c is None:
+        c = torch.empty((max(num_e, 0), m, n), dtype=torch.float32, device=dy.device)
+    if tuple(_contig(c, torch.float32, "c").shape) != (num_e, m, n):
+        raise ValueError("c must be [experts, m, n]")
+    _same_device(dy, (x, "x"), (seg_offsets, "seg_offsets"), (c, "c"))
+    _call("fp8bs_grouped_wgrad_ragged", dy.device, _on(dy.device, stream), dy.data_ptr(), ldy, x.data_ptr(), ldx,
+          seg_offsets.data_ptr(), num_e, rows, m, n, c.data_ptr(), int(accumulate))
+    return c

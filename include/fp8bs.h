@@ -69,7 +69,7 @@ extern "C" {
 #define FP8BS_ERR_ALIGN (-3)  /* a pointer or leading dimension is misaligned         */
 #define FP8BS_ERR_FLAG (-4)   /* an enum-like flag has an unknown value               */
 #define FP8BS_ERR_LAUNCH (-5) /* the HIP runtime rejected a kernel launch             */
-#define FP8BS_ERR_SCRATCH (-6) /* needs more than fp8bs_gemm_noalloc's fixed array     */
+#define FP8BS_ERR_SCRATCH (-6) /* needs more workspace than given, or than fp8bs_gemm_noalloc's fixed array */
 
 /*
  * Activation quantization in 1x128 tiles: one FP32 scale per row and 128
@@ -416,6 +416,121 @@ int fp8bs_moe_permute_quantize(const uint16_t* x, int64_t tokens, int64_t hidden
 int fp8bs_moe_combine(const uint16_t* y, int64_t ldy, int64_t rows_cap, const int32_t* slot_rows,
                       const float* gates, int64_t tokens, int64_t topk, int64_t n, uint16_t* out,
                       int64_t ldo, void* stream);
+
+/*
+ * ---- A linear layer's epilogue, forward and backward ------------------------
+ * The same FP8 products as fp8bs_gemm; everything around the matrix product
+ * stays in FP32 and bf16 (deepseek.csdn.net page, section 二(四): the
+ * precision-sensitive operations are kept in BF16 / FP32).
+ */
+#define FP8BS_ACT_NONE 0       /* act(z) = z                                          */
+#define FP8BS_ACT_RELU 1       /* max(z, 0)                                           */
+#define FP8BS_ACT_GELU_TANH 2  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))       */
+#define FP8BS_ACT_SILU 3       /* z / (1 + e^-z)                                      */
+
+/*
+ * fp8bs_gemm with a linear layer's epilogue:
+ *   z = A B + bias,   c = act(z) + residual
+ * bias, act and residual are applied to the FP32 accumulator; c is rounded to
+ * bf16 once (nearest, ties to even).  With z given, z is also stored, rounded
+ * to bf16, for fp8bs_epilogue_backward (act still sees the unrounded z).
+ *   qa, sa, qb, sb, m, n, k, b_layout, c, ldc: as for fp8bs_gemm
+ *   bias      f32 [n], or NULL (zero)
+ *   act       FP8BS_ACT_*
+ *   residual  bf16 [m, n], row stride ldr elements, or NULL; it may be c itself
+ *             (same pointer and stride), otherwise it must not overlap c or z
+ *   z         bf16 [m, n], row stride ldz elements, or NULL; must not overlap c
+ * ldr and ldz are ignored where their pointer is NULL.
+ * Alignment: as for fp8bs_gemm; residual and z 16 bytes, ldr and ldz % 8 == 0,
+ * bias 4 bytes.  Errors: FP8BS_ERR_FLAG for an unknown act.  Never allocates.
+ */
+int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t m,
+                        int64_t n, int64_t k, int b_layout, const float* bias, int act,
+                        const uint16_t* residual, int64_t ldr, uint16_t* z, int64_t ldz, uint16_t* c,
+                        int64_t ldc, void* stream);
+
+/*
+ * The epilogue's backward pass, from one read of dy and z:
+ *   dz[i, j] = dy[i, j] act'(z[i, j])  (bf16),   dbias[j] (+)= sum_i dz[i, j]  (f32)
+ * act' is taken at the stored bf16 z; relu'(0) = 0.  dbias sums the FP32 dz,
+ * before its rounding, in an order that depends on (m, n) only.  The residual's
+ * gradient is dy.
+ *   dy  bf16 [m, n], row stride ldy      z  bf16 [m, n], row stride ldz (may be
+ *       NULL with FP8BS_ACT_NONE, and is not read then)
+ *   dz  bf16 [m, n], row stride lddz, or NULL; may be dy or z themselves (same
+ *       pointer and stride), otherwise must not overlap them
+ *   dbias f32 [n] or NULL (not both NULL); accumulate == 1 adds to it
+ *   workspace  at least fp8bs_epilogue_backward_workspace(m, n) bytes, used only
+ *       by this call until it has run; may be NULL when that is 0 or dbias is NULL
+ *   m >= 1 (any), n % 8 == 0.
+ * Alignment: dy, z, dz 16 bytes, their strides % 8 == 0; dbias and workspace 4
+ * bytes.  Errors: FP8BS_ERR_SCRATCH when the workspace is missing or too small.
+ */
+int fp8bs_epilogue_backward(const uint16_t* dy, int64_t ldy, const uint16_t* z, int64_t ldz, int64_t m,
+                            int64_t n, int act, uint16_t* dz, int64_t lddz, float* dbias, int accumulate,
+                            float* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace fp8bs_epilogue_backward needs for dbias (host only; 0: none);
+ * FP8BS_ERR_SHAPE (negative) for sizes it refuses. */
+int64_t fp8bs_epilogue_backward_workspace(int64_t m, int64_t n);
+
+/*
+ * ---- Experts over segments of any length ------------------------------------
+ * The expert-major layout without padding: expert e owns rows [seg_offsets[e],
+ * seg_offsets[e+1]), of any length, zero included.  A decode step's few rows
+ * then stay few (64 pairs over 256 experts are 64 rows here, about 7400 in the
+ * 128-row layout of fp8bs_moe_route), and the training products run on the rows
+ * that carry tokens.  fp8bs_moe_permute_quantize and fp8bs_moe_combine take this
+ * layout as they are.  The segments of fp8bs_moe_route are a special case.
+ * seg_offsets (int32 [num_experts + 1], DEVICE memory) is expected to be
+ * non-decreasing within [0, total_rows]; offsets outside are clipped and a
+ * segment that runs backwards counts as empty, so no contents lead to an access
+ * outside the buffers.  Rows that belong to no segment are neither read nor
+ * written.
+ */
+
+/*
+ * fp8bs_moe_route without padding rows: the same stable order, segments end to
+ * end.  seg_offsets[num_experts] is the number of pairs kept; row_token [rows_cap]
+ * is -1 from there on.  rows_cap >= tokens * topk; the other arguments, sizes and
+ * errors as for fp8bs_moe_route.
+ */
+int fp8bs_moe_route_ragged(const int32_t* topk_ids, int64_t tokens, int64_t topk, int64_t num_experts,
+                           int32_t* seg_offsets, int32_t* slot_rows, int32_t* row_token, int64_t rows_cap,
+                           void* stream);
+
+/*
+ * Expert products over the segments: rows of expert e get fp8bs_gemm with that
+ * expert's weight, forward or activation gradient.
+ *   qa  E4M3 [total_rows, k] contiguous, sa f32 [total_rows, k/128] contiguous
+ *   b_layout == 0: qb E4M3 [num_experts, n, k], sb f32 [num_experts, n/128, k/128]
+ *   b_layout == 1: qb E4M3 [num_experts, k, n], sb f32 [num_experts, k/128, n/128]
+ *       (the forward weights as stored)
+ *   c   bf16 [total_rows, n], row stride ldc elements
+ *   1 <= num_experts <= 65536, 0 <= total_rows < 2^30 (0: nothing is done; qa,
+ *   sa and c may then be NULL), n % 128 == 0, k % 128 == 0; with b_layout 1,
+ *   k * n < 2^32 - 1.
+ * Alignment: qa, qb, c 16 bytes, ldc % 8 == 0, sa, sb, seg_offsets 4 bytes.
+ */
+int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets,
+                              int64_t num_experts, int64_t total_rows, const uint8_t* qb, const float* sb,
+                              int64_t n, int64_t k, int b_layout, uint16_t* c, int64_t ldc, void* stream);
+
+/*
+ * Experts' weight gradients over the segments, from bf16 rows:
+ *   c[e][i, j] (+)= sum over rows t of segment e of dy[t, i] x[t, j]   (f32)
+ * bf16 operands: a 128-token FP8 tile along the rows would cross experts here.
+ *   dy  bf16 [total_rows, m], row stride ldy     x  bf16 [total_rows, n], row stride ldx
+ *   c   f32 [num_experts, m, n] contiguous; accumulate == 0 overwrites every
+ *       expert's matrix (zeros for an empty segment), == 1 adds to it (an empty
+ *       segment's matrix is not touched)
+ *   1 <= num_experts <= 65536, 0 <= total_rows < 2^30 (0: dy and x may be NULL),
+ *   m % 8 == 0, n % 8 == 0, ldy, ldx <= 2^24.
+ * Alignment: dy, x, c 16 bytes, ldy and ldx % 8 == 0, seg_offsets 4 bytes.
+ */
+int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const uint16_t* x, int64_t ldx,
+                               const int32_t* seg_offsets, int64_t num_experts, int64_t total_rows, int64_t m,
+                               int64_t n, float* c, int accumulate, void* stream);
 
 /* Short English text for a status code (static storage, never NULL). */
 const char* fp8bs_status_string(int status);
