@@ -44,6 +44,7 @@
 //     and odd lanes at the same rows of columns n+8..n+15 leaves lane i with 8
 //     consecutive k of column n + i.
 
+#include <stdlib.h>
 #include <type_traits>
 
 #include "common.h"
@@ -927,7 +928,7 @@ __device__ __forceinline__ void copy_waves_bf16_weights(const GemmArgs& p, int c
 // activation-gradient B slab is stored as copied ([k][n], swz_t layout) and
 // gathered with ds_read_b64_tr_b8 as in gemm_kernel.
 // ---------------------------------------------------------------------------
-template <int MODE, int MW, int BM, int BN, bool PERSIST, bool SPLIT = false, bool W16 = false>
+template <int MODE, int MW, int BM, int BN, bool PERSIST, bool SPLIT = false, bool W16 = false, int VAR = kPlain>
 __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // MW MFMA waves: 4 (one per SIMD) or 8 (two per SIMD, so one wave's fold
   // VALU work runs under the other's MFMAs; register budget 168 per lane for
@@ -948,9 +949,11 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   constexpr int SB_JOBS = BN / 64;            // 64-column scale copies of B
   static_assert(MODE == kFprop || MODE == kDgrad || MODE == kWgrad || MODE == kGrouped, "mode");
   static_assert(MW == 4 || MW == 8, "MFMA wave count");
-  static_assert((BN == 128 && (BM == 256 || BM == 192)) ||
+  static_assert((BN == 128 && (BM == 256 || BM == 192 || (VAR == kRagged && BM == 128))) ||
                     ((BN == 256 || BN == 192) && BM == 128 && MODE != kDgrad),
                 "tile shape");
+  static_assert(VAR == kPlain || ((MODE == kFprop || MODE == kDgrad) && !SPLIT && !(VAR == kRagged && PERSIST)),
+                "variants of the bf16-output products");
   static_assert(WAVES_M * WAVES_N == MW && WM % 16 == 0, "whole MFMA tiles per wave");
   static_assert(!W16 || (MODE == kGrouped && !PERSIST && !SPLIT && BM == 128 && BN == 256 && MW == 8),
                 "bf16 weights: grouped 128 x 256 tiles");
@@ -971,7 +974,15 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // (u / nkb)-th tile.  The LDS ring and the barriers run across tile
   // boundaries, so the next tile's first slabs are copied while the MFMA
   // waves store the previous tile.
-  const int64_t M = p.m, N = p.n, K = p.k;
+  // ragged (one tile per workgroup, row-major): the segment's tile is found
+  // once, here, and M is the end of its rows
+  RaggedTile rt{0, 0, 0};
+  if constexpr (VAR == kRagged) {
+    const uint32_t tm = blockIdx.x / (uint32_t)p.tiles_n;
+    rt = ragged_tile(p.seg, (int)p.num_experts, p.m, (int)tm, BM, lane);
+    if (rt.e < 0) return;                      // more tiles in the grid than the segments hold
+  }
+  const int64_t M = VAR == kRagged ? rt.m0 + rt.rows : p.m, N = p.n, K = p.k;
   const int nkb = (int)(K / BK);               // K blocks of a row (the width of the scale rows)
   // SPLIT: workgroup (x, y) runs slabs [y * nslab, (y + 1) * nslab) of tile x
   // and stores its FP32 partial to ws[y]; a second kernel sums the partials
@@ -991,6 +1002,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   TileMN grouped_tile{0, 0};
   if constexpr (MODE == kGrouped) grouped_tile = tile_coords<W16 ? -3 : 0>(p, blockIdx.x);
   auto tile_origin = [&](int i) {
+    if constexpr (VAR == kRagged) return Origin{rt.m0, (int64_t)(blockIdx.x % (uint32_t)p.tiles_n) * BN};
     const TileMN t = MODE == kGrouped ? grouped_tile : tile_coords(p, (uint32_t)((int64_t)blockIdx.x + (int64_t)i * G));
     return Origin{(int64_t)t.m * BM, (int64_t)t.n * BN};
   };
@@ -1029,6 +1041,10 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       const int64_t rows_b = N - n0 < BN ? N - n0 : BN;
       const uint8_t* qb = p.qb;
       const float* sb = p.sb;
+      if (VAR == kRagged) {
+        qb += (int64_t)rt.e * N * K;
+        sb += (int64_t)rt.e * (N / 128) * nkb;
+      }
       if (MODE == kGrouped) {
         // expert whose segment holds row m0: the largest e with seg[e] <= m0
         int lo = 0, hi = (int)p.num_experts;
@@ -1355,6 +1371,8 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
           if (col < N)
             *reinterpret_cast<float4*>(prow + col) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
         }
+      } else if constexpr (VAR == kEpi) {
+        store_row_epi<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       } else if (MODE != kWgrad) {
         store_row_bf16<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       } else {
@@ -1427,7 +1445,7 @@ static int64_t persistent_grid(const GemmArgs& a, int cus) {
 // 64x96 patches read 29% less LDS per slab than two waves' 64x48 ones
 // (4096x1536x7168: 51.3 -> 49.9 us; with the single-slab A prefetch two
 // waves per SIMD had been faster, 61.5 against 56.7 us).
-template <int MODE, int MW>
+template <int MODE, int MW, int VAR = kPlain>
 static int launch_wide(GemmArgs a, hipStream_t s, int cus) {
   a.tiles_n = (a.n + 191) / 192;
   a.tiles_m = (a.m + 127) / 128;
@@ -1436,9 +1454,9 @@ static int launch_wide(GemmArgs a, hipStream_t s, int cus) {
   const int64_t grid = persistent_grid(a, cus);
   if (grid <= 0) return FP8BS_ERR_SHAPE;
   if (grid < tiles)
-    hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 128, 192, true>), dim3((unsigned)grid), dim3(64 * (MW + 4)), 0, s, a);
+    hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 128, 192, true, false, false, VAR>), dim3((unsigned)grid), dim3(64 * (MW + 4)), 0, s, a);
   else
-    hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 128, 192, false>), dim3((unsigned)grid), dim3(64 * (MW + 4)), 0, s, a);
+    hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 128, 192, false, false, false, VAR>), dim3((unsigned)grid), dim3(64 * (MW + 4)), 0, s, a);
   return launch_status();
 }
 
@@ -1452,12 +1470,12 @@ static int64_t tile_cost(int64_t m, int64_t n, int bm, int bn, int cost100, int 
   return ((tiles + cus - 1) / cus) * bm * bn * cost100;
 }
 
-template <int MODE>
+template <int MODE, int VAR = kPlain>
 static int launch_gemm_ws(GemmArgs a, hipStream_t s, int cus) {
   constexpr int MW = MODE == kWgrad ? 4 : 8;
   const int64_t c256 = tile_cost(a.m, a.n, 256, 128, 100, cus), c192 = tile_cost(a.m, a.n, 192, 128, 110, cus);
   if (MODE == kFprop && tile_cost(a.m, a.n, 128, 192, 121, cus) < (c256 < c192 ? c256 : c192))
-    return launch_wide<kFprop, 4>(a, s, cus);
+    return launch_wide<kFprop, 4, VAR>(a, s, cus);
   a.tiles_n = (a.n + 127) / 128;
   const bool tall = c256 <= c192;
   a.tiles_m = tall ? (a.m + 255) / 256 : (a.m + 191) / 192;
@@ -1474,14 +1492,14 @@ static int launch_gemm_ws(GemmArgs a, hipStream_t s, int cus) {
   // 4096 tokens: 101 -> 121 us)
   if (grid < tiles) {
     if (tall)
-      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 256, 128, true>), dim3((unsigned)grid), block, 0, s, a);
+      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 256, 128, true, false, false, VAR>), dim3((unsigned)grid), block, 0, s, a);
     else
-      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 192, 128, true>), dim3((unsigned)grid), block, 0, s, a);
+      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 192, 128, true, false, false, VAR>), dim3((unsigned)grid), block, 0, s, a);
   } else {
     if (tall)
-      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 256, 128, false>), dim3((unsigned)grid), block, 0, s, a);
+      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 256, 128, false, false, false, VAR>), dim3((unsigned)grid), block, 0, s, a);
     else
-      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 192, 128, false>), dim3((unsigned)grid), block, 0, s, a);
+      hipLaunchKernelGGL((gemm_ws_kernel<MODE, MW, 192, 128, false, false, false, VAR>), dim3((unsigned)grid), block, 0, s, a);
   }
   return launch_status();
 }
@@ -1502,6 +1520,18 @@ static int launch_grouped_ws(GemmArgs a, hipStream_t s) {
   // one tile per workgroup: the persistent form measured 9% slower here
   // (256 experts of 4096x7168), its in-loop store spilling registers
   hipLaunchKernelGGL((gemm_ws_kernel<kGrouped, 8, 128, 256, false, false, W16>), dim3((unsigned)grid),
+                     dim3(64 * 12), 0, s, a);
+  return launch_status();
+}
+
+// Ragged expert segments on BM x 128 tiles, row-major.
+template <int MODE, int BM>
+static int launch_ragged_ws(GemmArgs a, hipStream_t s) {
+  a.tiles_n = a.n / 128;
+  a.tiles_m = ragged_tiles(a.m, a.num_experts, BM);
+  const int64_t grid = a.tiles_m * a.tiles_n;
+  if (grid > kMaxGrid) return FP8BS_ERR_SHAPE;
+  hipLaunchKernelGGL((gemm_ws_kernel<MODE, 8, BM, 128, false, false, false, kRagged>), dim3((unsigned)grid),
                      dim3(64 * 12), 0, s, a);
   return launch_status();
 }
@@ -1645,14 +1675,15 @@ static bool split_grid_ok(int64_t m, int64_t n, int64_t ks) {
 // problem that use_ws turns away has fewer 128 x 128 tiles than CUs, since
 // those are at most twice its 192 x 128 tiles, so gemm_kernel's 128 x 128
 // tiles serve only the grouped GEMM.)
+template <int VAR = kPlain>
 static int gemm_unsplit(GemmArgs a, int b_layout, hipStream_t stream) {
   const int64_t m = a.m, n = a.n;
   if (use_ws(m, n, false)) {
-    if (b_layout == 0) return launch_gemm_ws<kFprop>(a, stream, cu_count());
-    return launch_gemm_ws<kDgrad>(a, stream, cu_count());
+    if (b_layout == 0) return launch_gemm_ws<kFprop, VAR>(a, stream, cu_count());
+    return launch_gemm_ws<kDgrad, VAR>(a, stream, cu_count());
   }
-  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL>(a, stream);
-  return launch_gemm<kDgrad, FP8BS_TILE_SMALL>(a, stream);
+  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, VAR>(a, stream);
+  return launch_gemm<kDgrad, FP8BS_TILE_SMALL, VAR>(a, stream);
 }
 
 // Argument checks of fp8bs_gemm; on success fills *a.
@@ -1870,8 +1901,7 @@ extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uin
     return FP8BS_ERR_ALIGN;
   a.epi = Epilogue{bias, residual, ldr, z, ldz, act};
   hipStream_t s = (hipStream_t)stream;
-  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, kEpi>(a, s);
-  return launch_gemm<kDgrad, FP8BS_TILE_SMALL, kEpi>(a, s);
+  return gemm_unsplit<kEpi>(a, b_layout, s);
 }
 
 extern "C" int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets,
@@ -1890,6 +1920,14 @@ extern "C" int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, con
   GemmArgs a{qa, sa, qb, sb, c, ldc, total_rows, n, k, seg_offsets, num_experts, 0, 0, 0, 0, nullptr, 1,
              total_rows * n * 2 > kStreamBytes};
   hipStream_t s = (hipStream_t)stream;
-  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, kRagged>(a, s);
-  return launch_gemm<kDgrad, FP8BS_TILE_SMALL, kRagged>(a, s);
+  const int64_t mean = total_rows / num_experts;
+  const char* ev = getenv("RG_BM");
+  int bm = ev ? atoi(ev) : (mean <= 40 ? 64 : mean <= 90 ? 128 : mean <= 160 ? 192 : 256);
+  if (bm == 64) {
+    if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, kRagged>(a, s);
+    return launch_gemm<kDgrad, FP8BS_TILE_SMALL, kRagged>(a, s);
+  }
+  if (bm == 128) return b_layout == 0 ? launch_ragged_ws<kFprop, 128>(a, s) : launch_ragged_ws<kDgrad, 128>(a, s);
+  if (bm == 192) return b_layout == 0 ? launch_ragged_ws<kFprop, 192>(a, s) : launch_ragged_ws<kDgrad, 192>(a, s);
+  return b_layout == 0 ? launch_ragged_ws<kFprop, 256>(a, s) : launch_ragged_ws<kDgrad, 256>(a, s);
 }

@@ -472,35 +472,46 @@ def fp8bs_moe_combine(y, slot_rows, gates, out=None, stream=None):
     return out
 
 
-def _same_device(ref, *named):
+_raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: a torch.cuda.Stream object costs 2 us
+
+
+def _on_device(dev, *named):
+    """Checks that the given tensors (or None) are on CUDA/HIP device index `dev`."""
     for t, nm in named:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{nm} must be on {ref.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{nm} must be on cuda:{dev}")
 
 
-def _on(device, stream):
-    """The stream of the call: the caller's, or the current one of the tensors' device."""
+def _call(fn, dev, stream, *args):
+    """Run entry point `fn` on the caller's stream or the current one of device index `dev`, with that
+    device current (kernels go to the current device)."""
     if stream is None:
-        return torch.cuda.current_stream(device)
-    if stream.device != device:
-        raise ValueError(f"the stream must belong to {device}")
-    return stream
+        handle = _raw_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"the stream must belong to cuda:{dev}")
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != FP8BS_OK:
+        raise Fp8bsError(fn.__name__, status)
 
 
-def _call(name, device, stream, *args):
-    """Run entry point `name` with the tensors' device current (kernels go to the current device)."""
-    with torch.cuda.device(device):
-        _check(name, getattr(raw, name)(*args, ctypes.c_void_p(stream.cuda_stream)))
-
-
-def _matrix(t, dtype, shape, name):
+def _matrix(t, dtype, rows, cols, name):
     """Checks a [rows, cols] tensor with unit column stride; returns its row stride.
 
-    A tensor of one row has that row's length as its stride whatever torch reports."""
+    A single row's stride says nothing about it: it counts as the row's length."""
     _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape) or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be {list(shape)} with unit column stride")
-    return t.stride(0) if shape[0] > 1 else max(shape[1], 8 * -(-shape[1] // 8))
+    if t.shape != (rows, cols) or (t.stride(1) != 1 and cols > 1):
+        raise ValueError(f"{name} must be [{rows}, {cols}] with unit column stride")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def fp8bs_gemm_epilogue(qa, sa, qb, sb, b_layout=0, bias=None, act=FP8BS_ACT_NONE, residual=None, z=None, c=None,
@@ -520,20 +531,19 @@ def fp8bs_gemm_epilogue(qa, sa, qb, sb, b_layout=0, bias=None, act=FP8BS_ACT_NON
     m, k = qa.shape
     n, kb = (qb.shape[0], qb.shape[1]) if b_layout == 0 else (qb.shape[1], qb.shape[0])
     blocks = (qb.shape[0] // GROUP, qb.shape[1] // GROUP)
-    if kb != k or tuple(sa.shape) != (m, k // GROUP) or tuple(sb.shape) != blocks:
+    if kb != k or sa.shape != (m, k // GROUP) or sb.shape != blocks:
         raise ValueError("operand and scale shapes do not match")
     if c is None:
         c = torch.empty((m, n), dtype=torch.bfloat16, device=qa.device)
-    ldc = _matrix(c, torch.bfloat16, (m, n), "c")
-    ldr = _matrix(residual, torch.bfloat16, (m, n), "residual") if residual is not None else 0
-    ldz = _matrix(z, torch.bfloat16, (m, n), "z") if z is not None else 0
-    if bias is not None and tuple(_contig(bias, torch.float32, "bias").shape) != (n,):
+    ldc = _matrix(c, torch.bfloat16, m, n, "c")
+    ldr = _matrix(residual, torch.bfloat16, m, n, "residual") if residual is not None else 0
+    ldz = _matrix(z, torch.bfloat16, m, n, "z") if z is not None else 0
+    if bias is not None and _contig(bias, torch.float32, "bias").shape != (n,):
         raise ValueError("bias must be [n]")
-    _same_device(qa, (sa, "sa"), (qb, "qb"), (sb, "sb"), (bias, "bias"), (residual, "residual"), (z, "z"), (c, "c"))
-    _call("fp8bs_gemm_epilogue", qa.device, _on(qa.device, stream), qa.data_ptr(), sa.data_ptr(), qb.data_ptr(),
-          sb.data_ptr(), m, n, k, b_layout, None if bias is None else bias.data_ptr(), int(act),
-          None if residual is None else residual.data_ptr(), ldr, None if z is None else z.data_ptr(), ldz,
-          c.data_ptr(), ldc)
+    dev = qa.get_device()
+    _on_device(dev, (sa, "sa"), (qb, "qb"), (sb, "sb"), (bias, "bias"), (residual, "residual"), (z, "z"), (c, "c"))
+    _call(raw.fp8bs_gemm_epilogue, dev, stream, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), m, n, k,
+          b_layout, _ptr(bias), act, _ptr(residual), ldr, _ptr(z), ldz, c.data_ptr(), ldc)
     return c
 
 
@@ -556,33 +566,31 @@ def fp8bs_epilogue_backward(dy, z, act=FP8BS_ACT_NONE, dz=None, dbias=None, accu
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
         raise ValueError("dy must be a bf16 matrix")
     m, n = dy.shape
-    dev = dy.device
-    ldy = _matrix(dy, torch.bfloat16, (m, n), "dy")
+    ldy = _matrix(dy, torch.bfloat16, m, n, "dy")
     ldz = 0
     if z is not None:
-        ldz = _matrix(z, torch.bfloat16, (m, n), "z")
+        ldz = _matrix(z, torch.bfloat16, m, n, "z")
     elif act != FP8BS_ACT_NONE:
         raise ValueError("z is needed for this activation")
     if accumulate and not isinstance(dbias, torch.Tensor):
         raise ValueError("accumulate needs a dbias to add to")
-    dz = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if dz is None else (None if dz is False else dz)
-    dbias = torch.empty(n, dtype=torch.float32, device=dev) if dbias is None else (None if dbias is False else dbias)
-    lddz = _matrix(dz, torch.bfloat16, (m, n), "dz") if dz is not None else 0
-    if dbias is not None and tuple(_contig(dbias, torch.float32, "dbias").shape) != (n,):
+    dz = torch.empty((m, n), dtype=torch.bfloat16, device=dy.device) if dz is None else (None if dz is False else dz)
+    dbias = torch.empty(n, dtype=torch.float32, device=dy.device) if dbias is None else (None if dbias is False else dbias)
+    lddz = _matrix(dz, torch.bfloat16, m, n, "dz") if dz is not None else 0
+    if dbias is not None and _contig(dbias, torch.float32, "dbias").shape != (n,):
         raise ValueError("dbias must be [n]")
-    s = _on(dev, stream)
-    need = fp8bs_epilogue_backward_workspace(m, n) if dbias is not None else 0
-    if workspace is None and need:
-        workspace = torch.empty(need // 4, dtype=torch.float32, device=dev)
-        if stream is not None:
-            workspace.record_stream(s)         # kept until that stream has used it
-    if workspace is not None:
+    if workspace is None and dbias is not None:
+        need = fp8bs_epilogue_backward_workspace(m, n)
+        if need:
+            workspace = torch.empty(need // 4, dtype=torch.float32, device=dy.device)
+            if stream is not None:
+                workspace.record_stream(stream)    # kept until that stream has used it
+    elif workspace is not None:
         _contig(workspace, torch.float32, "workspace")
-    _same_device(dy, (z, "z"), (dz, "dz"), (dbias, "dbias"), (workspace, "workspace"))
-    _call("fp8bs_epilogue_backward", dev, s, dy.data_ptr(), ldy, None if z is None else z.data_ptr(), ldz, m, n,
-          int(act), None if dz is None else dz.data_ptr(), lddz, None if dbias is None else dbias.data_ptr(),
-          int(accumulate), None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else 4 * workspace.numel())
+    dev = dy.get_device()
+    _on_device(dev, (z, "z"), (dz, "dz"), (dbias, "dbias"), (workspace, "workspace"))
+    _call(raw.fp8bs_epilogue_backward, dev, stream, dy.data_ptr(), ldy, _ptr(z), ldz, m, n, act, _ptr(dz), lddz,
+          _ptr(dbias), accumulate, _ptr(workspace), 0 if workspace is None else 4 * workspace.numel())
     return dz, dbias
 
 
@@ -610,8 +618,8 @@ def fp8bs_moe_route_ragged(topk_ids, num_experts, rows_cap=None, seg_offsets=Non
     if seg_offsets.numel() != num_experts + 1 or tuple(slot_rows.shape) != (tokens, topk) \
             or row_token.numel() != rows_cap:
         raise ValueError("output shapes do not match the routing")
-    _same_device(topk_ids, *outs)
-    _call("fp8bs_moe_route_ragged", dev, _on(dev, stream), topk_ids.data_ptr(), tokens, topk, num_experts,
+    _on_device(topk_ids.get_device(), *outs)
+    _call(raw.fp8bs_moe_route_ragged, topk_ids.get_device(), stream, topk_ids.data_ptr(), tokens, topk, num_experts,
           seg_offsets.data_ptr(), slot_rows.data_ptr(), row_token.data_ptr(), rows_cap)
     return seg_offsets, slot_rows, row_token
 
@@ -635,15 +643,16 @@ def fp8bs_grouped_gemm_ragged(qa, sa, seg_offsets, qb, sb, b_layout=0, c=None, s
     num_e = qb.shape[0]
     n, kb = (qb.shape[1], qb.shape[2]) if b_layout == 0 else (qb.shape[2], qb.shape[1])
     blocks = (num_e, qb.shape[1] // GROUP, qb.shape[2] // GROUP)
-    if kb != k or tuple(sa.shape) != (rows, k // GROUP) or tuple(sb.shape) != blocks:
+    if kb != k or sa.shape != (rows, k // GROUP) or sb.shape != blocks:
         raise ValueError("operand and scale shapes do not match")
     if seg_offsets.numel() != num_e + 1:
         raise ValueError("seg_offsets must have num_experts + 1 entries")
     if c is None:
         c = torch.empty((rows, n), dtype=torch.bfloat16, device=qa.device)
-    ldc = _matrix(c, torch.bfloat16, (rows, n), "c")
-    _same_device(qa, (sa, "sa"), (qb, "qb"), (sb, "sb"), (seg_offsets, "seg_offsets"), (c, "c"))
-    _call("fp8bs_grouped_gemm_ragged", qa.device, _on(qa.device, stream), qa.data_ptr(), sa.data_ptr(),
+    ldc = _matrix(c, torch.bfloat16, rows, n, "c")
+    dev = qa.get_device()
+    _on_device(dev, (sa, "sa"), (qb, "qb"), (sb, "sb"), (seg_offsets, "seg_offsets"), (c, "c"))
+    _call(raw.fp8bs_grouped_gemm_ragged, dev, stream, qa.data_ptr(), sa.data_ptr(),
           seg_offsets.data_ptr(), num_e, rows, qb.data_ptr(), sb.data_ptr(), n, k, b_layout, c.data_ptr(), ldc)
     return c
 
@@ -656,17 +665,18 @@ def fp8bs_grouped_wgrad_ragged(dy, x, seg_offsets, c=None, accumulate=0, stream=
         raise ValueError("dy and x must be bf16 matrices")
     rows, m = dy.shape
     n = x.shape[1]
-    ldy = _matrix(dy, torch.bfloat16, (rows, m), "dy")
-    ldx = _matrix(x, torch.bfloat16, (rows, n), "x")
+    ldy = _matrix(dy, torch.bfloat16, rows, m, "dy")
+    ldx = _matrix(x, torch.bfloat16, rows, n, "x")
     _contig(seg_offsets, torch.int32, "seg_offsets")
     num_e = seg_offsets.numel() - 1
     if accumulate and c is None:
         raise ValueError("accumulate needs a c to add to")
     if c is None:
         c = torch.empty((max(num_e, 0), m, n), dtype=torch.float32, device=dy.device)
-    if tuple(_contig(c, torch.float32, "c").shape) != (num_e, m, n):
+    if _contig(c, torch.float32, "c").shape != (num_e, m, n):
         raise ValueError("c must be [experts, m, n]")
-    _same_device(dy, (x, "x"), (seg_offsets, "seg_offsets"), (c, "c"))
-    _call("fp8bs_grouped_wgrad_ragged", dy.device, _on(dy.device, stream), dy.data_ptr(), ldy, x.data_ptr(), ldx,
-          seg_offsets.data_ptr(), num_e, rows, m, n, c.data_ptr(), int(accumulate))
+    dev = dy.get_device()
+    _on_device(dev, (x, "x"), (seg_offsets, "seg_offsets"), (c, "c"))
+    _call(raw.fp8bs_grouped_wgrad_ragged, dev, stream, dy.data_ptr(), ldy, x.data_ptr(), ldx,
+          seg_offsets.data_ptr(), num_e, rows, m, n, c.data_ptr(), accumulate)
     return c
