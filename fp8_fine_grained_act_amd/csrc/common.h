@@ -13,6 +13,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 
 constexpr int kGroup = 128;           // scale-group length along the contraction
+constexpr int BK = 128;               // contraction depth of a GEMM slab: one scale group
 constexpr float kE4M3Max = 448.0f;
 
 // x / s is evaluated as q = fma(x, r, x * rl) with r = 1/s correctly rounded
@@ -227,6 +228,52 @@ __device__ __forceinline__ uint4 load_nt(const void* p) {
   const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
   return make_uint4(w.x, w.y, w.z, w.w);
 }
+
+// The tile of `bm` rows with index `tm` when every expert's segment is cut into
+// ceil(length / bm) tiles, experts in order: its expert (-1: none, tm is past
+// the last tile), first row and row count.  The whole wave works on it: 64
+// experts per step, their tile counts summed by a scan.  Offsets are clipped to
+// [0, total_rows] and a segment that runs backwards counts as empty, so no
+// device contents lead to a row outside the buffers.
+struct RaggedTile {
+  int e;
+  int64_t m0, rows;
+};
+__device__ __forceinline__ RaggedTile ragged_tile(const int32_t* __restrict__ seg, int num_experts, int64_t total_rows,
+                                                  int tm, int bm, int lane) {
+  const int cap = (int)total_rows;
+  int done = 0;
+  for (int base = 0; base < num_experts; base += 64) {
+    const int e = base + lane;
+    int s0 = 0, len = 0;
+    if (e < num_experts) {
+      s0 = min(max(seg[e], 0), cap);
+      len = max(0, min(max(seg[e + 1], 0), cap) - s0);
+    }
+    const int tiles = (len + bm - 1) / bm;
+    int incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
+    }
+    const uint64_t hit = __ballot(done + incl > tm);
+    if (hit) {
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      const int i = tm - done - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l));
+      const int left = __builtin_amdgcn_readlane(len, l) - i * bm;
+      if (i < 0 || left <= 0) break;
+      return RaggedTile{base + l, (int64_t)__builtin_amdgcn_readlane(s0, l) + (int64_t)i * bm, min(left, bm)};
+    }
+    done += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return RaggedTile{-1, 0, 0};
+}
+
+// The dgrad weight slab in LDS (rows = k, 128 bytes): chunk c of row r is stored
+// at c ^ swz_ht(r); see the bank layout in gemm.hip.
+__device__ __forceinline__ int swz_ht(int row) { return ((row >> 1) & 3) | ((row >> 3) & 4); }
+__device__ __forceinline__ int swz_t(int row, int chunk) { return row * BK + ((chunk ^ swz_ht(row)) << 4); }
 
 // ---- buffer copies straight into LDS, and vmcnt waits ---------------------
 constexpr int kRsrcWord3 = 0x00020000;  // raw (untyped) buffer access, gfx9 family

@@ -44,11 +44,13 @@
 //     and odd lanes at the same rows of columns n+8..n+15 leaves lane i with 8
 //     consecutive k of column n + i.
 
-#include <stdlib.h>
+#include <math.h>
+
 #include <type_traits>
 
 #include "common.h"
 #include "launch.h"
+#include "skinny.h"
 
 namespace fp8bs {
 
@@ -163,48 +165,6 @@ __device__ inline TileMN tile_coords(const GemmArgs& p, uint32_t b) {
   return TileMN{first + (r - n * rows), n};
 }
 
-// The tile of `bm` rows with index `tm` when every expert's segment is cut into
-// ceil(length / bm) tiles, experts in order: its expert (-1: none, tm is past
-// the last tile), first row and row count.  The whole wave works on it: 64
-// experts per step, their tile counts summed by a scan.  Offsets are clipped to
-// [0, total_rows] and a segment that runs backwards counts as empty, so no
-// device contents lead to a row outside the buffers.
-struct RaggedTile {
-  int e;
-  int64_t m0, rows;
-};
-__device__ __forceinline__ RaggedTile ragged_tile(const int32_t* __restrict__ seg, int num_experts, int64_t total_rows,
-                                                  int tm, int bm, int lane) {
-  const int cap = (int)total_rows;
-  int done = 0;
-  for (int base = 0; base < num_experts; base += 64) {
-    const int e = base + lane;
-    int s0 = 0, len = 0;
-    if (e < num_experts) {
-      s0 = min(max(seg[e], 0), cap);
-      len = max(0, min(max(seg[e + 1], 0), cap) - s0);
-    }
-    const int tiles = (len + bm - 1) / bm;
-    int incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(incl, d);
-      if (lane >= d) incl += o;
-    }
-    const uint64_t hit = __ballot(done + incl > tm);
-    if (hit) {
-      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-      const int i = tm - done - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l));
-      const int left = __builtin_amdgcn_readlane(len, l) - i * bm;
-      if (i < 0 || left <= 0) break;
-      return RaggedTile{base + l, (int64_t)__builtin_amdgcn_readlane(s0, l) + (int64_t)i * bm, min(left, bm)};
-    }
-    done += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return RaggedTile{-1, 0, 0};
-}
-
-constexpr int BK = 128;
 // LDS bank layout, measured on gfx950 (bank-conflict counter, one lane pair
 // at a time): 64 banks of 4 bytes; ds_read_b128 serves 16 lanes per pass,
 // lanes 0-3, 12-15, 20-23 and 24-27 forming one pass (within each half
@@ -223,11 +183,9 @@ constexpr int BK = 128;
 // read patterns alone: 202 B/clk/CU for the fragment reads (113 with the
 // earlier (r >> 1) & 7), 147 for the transposing reads (112).
 __device__ __forceinline__ int swz_h(int row) { return (row >> 1) & 5; }
-__device__ __forceinline__ int swz_ht(int row) { return ((row >> 1) & 3) | ((row >> 3) & 4); }
 // byte offset of 16-byte chunk `chunk` of LDS row `row`, fragment layout
 __device__ __forceinline__ int swz(int row, int chunk) { return row * BK + ((chunk ^ swz_h(row)) << 4); }
-// the same in the dgrad weight layout
-__device__ __forceinline__ int swz_t(int row, int chunk) { return row * BK + ((chunk ^ swz_ht(row)) << 4); }
+// (the dgrad weight layout's swz_ht and swz_t are in common.h)
 
 
 
@@ -388,7 +346,7 @@ __device__ __forceinline__ void store_row_epi(const GemmArgs& p, const v4f (&acc
 template <int MODE, int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int VAR = kPlain>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) __attribute__((amdgpu_waves_per_eu(1, 2)))
 void gemm_kernel(GemmArgs p) {
-  static_assert(VAR == kPlain || MODE == kFprop || MODE == kDgrad, "variants of the bf16-output products");
+  static_assert(VAR == kPlain || (VAR == kRagged && (MODE == kFprop || MODE == kDgrad)), "plain, or ragged segments");
   using C = GemmCfg<MODE, BM, BN, WAVES_M, WAVES_N, STAGES>;
   constexpr int WM = C::WM, WN = C::WN, TM = C::TM, TN = C::TN;
   constexpr int NW = C::kWaves;
@@ -622,10 +580,6 @@ void gemm_kernel(GemmArgs p) {
   for (int j = 0; j < TM; ++j) {
     const int64_t row = m0 + WM * wm + 16 * j + l16;
     if (row >= M) continue;
-    if (VAR == kEpi) {
-      store_row_epi<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
-      continue;
-    }
     if (MODE != kWgrad) {
       store_row_bf16<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       continue;
@@ -685,12 +639,6 @@ static int64_t choose_group_m(const GemmArgs& a, int64_t bm, int64_t bn, int64_t
     if (best_cost < 0 || c < best_cost) best = gm, best_cost = c;
   }
   return best;
-}
-
-// Most tiles of bm rows that segments of at most `rows` rows in all can need:
-// every expert that owns a row may leave one tile partly filled.
-static int64_t ragged_tiles(int64_t rows, int64_t num_experts, int64_t bm) {
-  return (rows + (bm - 1) * (num_experts < rows ? num_experts : rows)) / bm;
 }
 
 template <int MODE, int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int VAR = kPlain>
@@ -949,7 +897,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   constexpr int SB_JOBS = BN / 64;            // 64-column scale copies of B
   static_assert(MODE == kFprop || MODE == kDgrad || MODE == kWgrad || MODE == kGrouped, "mode");
   static_assert(MW == 4 || MW == 8, "MFMA wave count");
-  static_assert((BN == 128 && (BM == 256 || BM == 192 || (VAR == kRagged && BM == 128))) ||
+  static_assert((BN == 128 && (BM == 256 || BM == 192 || (VAR != kPlain && BM == 128))) ||
                     ((BN == 256 || BN == 192) && BM == 128 && MODE != kDgrad),
                 "tile shape");
   static_assert(VAR == kPlain || ((MODE == kFprop || MODE == kDgrad) && !SPLIT && !(VAR == kRagged && PERSIST)),
@@ -1524,16 +1472,45 @@ static int launch_grouped_ws(GemmArgs a, hipStream_t s) {
   return launch_status();
 }
 
-// Ragged expert segments on BM x 128 tiles, row-major.
-template <int MODE, int BM>
-static int launch_ragged_ws(GemmArgs a, hipStream_t s) {
+// BM x 128 tiles, one per workgroup: ragged expert segments (row-major), and a
+// linear layer with fewer tiles than CUs.
+template <int MODE, int BM, int VAR>
+static int launch_ws_tiles(GemmArgs a, hipStream_t s) {
   a.tiles_n = a.n / 128;
-  a.tiles_m = ragged_tiles(a.m, a.num_experts, BM);
+  a.tiles_m = VAR == kRagged ? ragged_tiles(a.m, a.num_experts, BM) : (a.m + BM - 1) / BM;
+  a.group_m = VAR == kRagged ? -1 : choose_group_m(a, BM, 128, 2);
   const int64_t grid = a.tiles_m * a.tiles_n;
   if (grid > kMaxGrid) return FP8BS_ERR_SHAPE;
-  hipLaunchKernelGGL((gemm_ws_kernel<MODE, 8, BM, 128, false, false, false, kRagged>), dim3((unsigned)grid),
-                     dim3(64 * 12), 0, s, a);
+  hipLaunchKernelGGL((gemm_ws_kernel<MODE, 8, BM, 128, false, false, false, VAR>), dim3((unsigned)grid), dim3(64 * 12), 0,
+                     s, a);
   return launch_status();
+}
+
+// Tile height for ragged segments: 64 (gemm_kernel, two workgroups per CU), 128,
+// 192 or 256 (warp-specialized), by rounds of the chip times what a round costs.
+// The rows' distribution is on the device; the estimate takes each expert that
+// can own rows two standard deviations (of a Poisson count) above the mean.
+// Costs per round (us over 32 blocks, measured with one tile per CU, and two
+// for the 64-row tiles).  Measured choices: 256 experts of 4096 x 7168 with 128
+// rows each 2.39 / 2.22 / 1.96 / 2.08 ms on 64 / 128 / 192 / 256 rows; 64 experts
+// of 7168 x 4096 (dgrad) with 187 rows 834 / 760 / 670 / 619 us; 256 experts of
+// 2048 x 2048 with 2 rows 157 / 196 us on 64 / 128 rows.
+static int ragged_tile_rows(int64_t rows, int64_t num_experts, int64_t n, int64_t cus) {
+  const int64_t owners = num_experts < rows ? num_experts : rows;
+  const double mean = (double)rows / (double)owners;
+  const double high = owners == 1 ? mean : mean + 2.0 * sqrt(mean);
+  constexpr struct {
+    int bm, per_cu;
+    double cost;
+  } kTiles[] = {{64, 2, 21.0}, {128, 1, 13.0}, {192, 1, 17.5}, {256, 1, 22.0}};
+  int best = 64;
+  double best_cost = 0.0;
+  for (const auto& t : kTiles) {
+    const double tiles = (double)owners * ceil(high / t.bm) * (double)(n / 128);
+    const double c = ceil(tiles / (double)(t.per_cu * cus)) * t.cost;
+    if (t.bm == 64 || c < best_cost) best = t.bm, best_cost = c;
+  }
+  return best;
 }
 
 }  // namespace fp8bs
@@ -1675,15 +1652,14 @@ static bool split_grid_ok(int64_t m, int64_t n, int64_t ks) {
 // problem that use_ws turns away has fewer 128 x 128 tiles than CUs, since
 // those are at most twice its 192 x 128 tiles, so gemm_kernel's 128 x 128
 // tiles serve only the grouped GEMM.)
-template <int VAR = kPlain>
 static int gemm_unsplit(GemmArgs a, int b_layout, hipStream_t stream) {
   const int64_t m = a.m, n = a.n;
   if (use_ws(m, n, false)) {
-    if (b_layout == 0) return launch_gemm_ws<kFprop, VAR>(a, stream, cu_count());
-    return launch_gemm_ws<kDgrad, VAR>(a, stream, cu_count());
+    if (b_layout == 0) return launch_gemm_ws<kFprop>(a, stream, cu_count());
+    return launch_gemm_ws<kDgrad>(a, stream, cu_count());
   }
-  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, VAR>(a, stream);
-  return launch_gemm<kDgrad, FP8BS_TILE_SMALL, VAR>(a, stream);
+  if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL>(a, stream);
+  return launch_gemm<kDgrad, FP8BS_TILE_SMALL>(a, stream);
 }
 
 // Argument checks of fp8bs_gemm; on success fills *a.
@@ -1888,6 +1864,10 @@ extern "C" int fp8bs_gemm_wgrad(const uint8_t* qa, const float* sa, const uint8_
   return launch_gemm<kWgrad, FP8BS_TILE_SMALL>(a, s);
 }
 
+// What a round of the 128 x 128 warp-specialized tiles takes, in skinny.h's unit
+// (a product that use_ws turns away has at most one such tile per CU).
+constexpr int64_t kTile128Cost = 23;
+
 extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb,
                                    int64_t m, int64_t n, int64_t k, int b_layout, const float* bias, int act,
                                    const uint16_t* residual, int64_t ldr, uint16_t* z, int64_t ldz, uint16_t* c,
@@ -1901,7 +1881,12 @@ extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uin
     return FP8BS_ERR_ALIGN;
   a.epi = Epilogue{bias, residual, ldr, z, ldz, act};
   hipStream_t s = (hipStream_t)stream;
-  return gemm_unsplit<kEpi>(a, b_layout, s);
+  const int64_t cus = cu_count();
+  if (use_ws(m, n, false))
+    return b_layout == 0 ? launch_gemm_ws<kFprop, kEpi>(a, s, cus) : launch_gemm_ws<kDgrad, kEpi>(a, s, cus);
+  const SkinnyArgs sk{qa, sa, qb, sb, c, ldc, m, n, k, nullptr, 1, a.epi};
+  if (skinny_cost(sk, b_layout, cus) <= kTile128Cost) return launch_skinny(sk, b_layout, cus, s);
+  return b_layout == 0 ? launch_ws_tiles<kFprop, 128, kEpi>(a, s) : launch_ws_tiles<kDgrad, 128, kEpi>(a, s);
 }
 
 extern "C" int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets,
@@ -1920,14 +1905,15 @@ extern "C" int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, con
   GemmArgs a{qa, sa, qb, sb, c, ldc, total_rows, n, k, seg_offsets, num_experts, 0, 0, 0, 0, nullptr, 1,
              total_rows * n * 2 > kStreamBytes};
   hipStream_t s = (hipStream_t)stream;
-  const int64_t mean = total_rows / num_experts;
-  const char* ev = getenv("RG_BM");
-  int bm = ev ? atoi(ev) : (mean <= 40 ? 64 : mean <= 90 ? 128 : mean <= 160 ? 192 : 256);
-  if (bm == 64) {
-    if (b_layout == 0) return launch_gemm<kFprop, FP8BS_TILE_SMALL, kRagged>(a, s);
-    return launch_gemm<kDgrad, FP8BS_TILE_SMALL, kRagged>(a, s);
+  const int64_t cus = cu_count();
+  const SkinnyArgs sk{qa, sa, qb, sb, c, ldc, total_rows, n, k, seg_offsets, num_experts, Epilogue{}};
+  if (skinny_cost(sk, b_layout, cus) < kTile128Cost) return launch_skinny(sk, b_layout, cus, s);
+  const bool fwd = b_layout == 0;
+  switch (ragged_tile_rows(total_rows, num_experts, n, cus)) {
+    case 64:
+      return fwd ? launch_gemm<kFprop, FP8BS_TILE_SMALL, kRagged>(a, s) : launch_gemm<kDgrad, FP8BS_TILE_SMALL, kRagged>(a, s);
+    case 128: return fwd ? launch_ws_tiles<kFprop, 128, kRagged>(a, s) : launch_ws_tiles<kDgrad, 128, kRagged>(a, s);
+    case 192: return fwd ? launch_ws_tiles<kFprop, 192, kRagged>(a, s) : launch_ws_tiles<kDgrad, 192, kRagged>(a, s);
+    default: return fwd ? launch_ws_tiles<kFprop, 256, kRagged>(a, s) : launch_ws_tiles<kDgrad, 256, kRagged>(a, s);
   }
-  if (bm == 128) return b_layout == 0 ? launch_ragged_ws<kFprop, 128>(a, s) : launch_ragged_ws<kDgrad, 128>(a, s);
-  if (bm == 192) return b_layout == 0 ? launch_ragged_ws<kFprop, 192>(a, s) : launch_ragged_ws<kDgrad, 192>(a, s);
-  return b_layout == 0 ? launch_ragged_ws<kFprop, 256>(a, s) : launch_ragged_ws<kDgrad, 256>(a, s);
 }

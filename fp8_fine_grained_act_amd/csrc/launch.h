@@ -44,4 +44,10 @@ inline int cu_count() {
   return n;
 }
 
+// Most tiles of bm rows that segments of at most `rows` rows in all can need:
+// every expert that owns a row may leave one tile partly filled.
+inline int64_t ragged_tiles(int64_t rows, int64_t num_experts, int64_t bm) {
+  return (rows + (bm - 1) * (num_experts < rows ? num_experts : rows)) / bm;
+}
+
 }  // namespace fp8bs

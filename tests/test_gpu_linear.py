@@ -252,3 +252,27 @@ def test_backward_graph_replays(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(dz.view(torch.int16), dz2.view(torch.int16)) and torch.equal(db, db2)
+
+
+@pytest.mark.parametrize("b_layout", [0, 1])
+@pytest.mark.parametrize("m,n,k", [(500, 1536, 1024), (1000, 1536, 512), (1100, 2048, 256), (2048, 2048, 512),
+                                   (1037, 7168, 256), (4096, 4096, 256), (4096, 1536, 384), (3000, 8192, 128),
+                                   (16, 8192, 256), (40, 7168, 384), (250, 2048, 640)])
+def test_epilogue_on_every_tile_shape(gpu_lib, m, n, k, b_layout):
+    """Products over one round of the chip and more: every tile shape, persistent workgroups, ragged last tiles."""
+    g = gen(m + n + k)
+    ops = operands(g, m, n, k, b_layout)
+    bias, res = normal(g, n), normal(g, m, n).bfloat16()
+    dev = [t.cuda() for t in ops]
+    z = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    c = gpu_lib.fp8bs_gemm_epilogue(*dev, b_layout=b_layout, bias=bias.cuda(), act=ACTS["gelu_tanh"], residual=res.cuda(),
+                                    z=z)
+    torch.cuda.synchronize()
+    z64, ez = product64(*dev, b_layout)
+    z64, ez = z64.cpu(), ez.cpu()
+    z64 = z64 + bias.double()
+    ez = ez + 2.0 ** -24 * (z64.abs() + ez)
+    y = act64(z64, "gelu_tanh") + res.double()
+    ey = SLOPE * ez + (argument(z64, "gelu_tanh") + 4) * 2.0 ** -24 * z64.abs()
+    check(z, z64, ez, "z")
+    check(c, y, ey + 2.0 ** -24 * (y.abs() + ey), "c")

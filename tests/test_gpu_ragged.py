@@ -262,3 +262,24 @@ def test_streams_and_graph(gpu_lib):
             u, v = b0[name], b1[name]
             assert torch.equal(u.view(torch.uint8), v.view(torch.uint8)), (i, name)
         assert torch.equal(b0["q"][:total], b1["q"][:total])
+
+
+@pytest.mark.parametrize("b_layout", [0, 1])
+@pytest.mark.parametrize("low,high,n", [(0, 8, 2048), (40, 80, 1024), (100, 150, 1024), (190, 256, 1024), (0, 600, 1024)])
+def test_every_tile_height(gpu_lib, low, high, n, b_layout):
+    """64 experts with few to many rows each: every tile height that the call chooses among."""
+    rng = np.random.default_rng(low + high)
+    lengths = [int(v) for v in rng.integers(low, high + 1, 64)]
+    lengths[5], lengths[63] = 0, high
+    k, e, g = 384, 64, gen(high)
+    seg = seg_of(lengths)
+    qa, sa = row_tiles(normal(g, int(seg[-1]), k))
+    qb, sb = blocks(normal(g, *((e, n, k) if b_layout == 0 else (e, k, n))) * 0.05)
+    dev = [t.cuda() for t in (qa, sa, qb, sb)]
+    c = gpu_lib.fp8bs_grouped_gemm_ragged(dev[0], dev[1], seg.cuda(), dev[2], dev[3], b_layout=b_layout)
+    torch.cuda.synchronize()
+    for i in range(e):
+        cut = slice(int(seg[i]), int(seg[i + 1]))
+        if cut.start < cut.stop:
+            y, err = product64(dev[0][cut], dev[1][cut], dev[2][i], dev[3][i], b_layout)
+            check(c[cut], y.cpu(), err.cpu(), f"expert {i}, {lengths[i]} rows")
