@@ -8,18 +8,29 @@
 // in FP32 and the matrix cores add them in FP32.
 //
 // Both operands have the contraction (rows t) as their slow index.  A slab of
-// kT rows by 128 columns of each is copied as it lies straight into LDS
+// kT rows by BM (dy) and BN (x) columns is copied as it lies straight into LDS
 // (buffer_load ... lds); the fragments, which need consecutive t per lane, are
 // gathered with ds_read_b64_tr_b16: in a group of 16 lanes that each point at 4
 // bf16, lane i receives element i mod 4 of the words of lanes 4r + i div 4, r =
 // 0..3; lane j therefore points at row t = 8g + j div 4 (+ 4 for the second
 // read), columns 4 (j mod 4) of the tile's 16, and lane i ends with column i at
 // t = 8g .. 8g + 7.
-// LDS rows are 256 bytes = 8 units of 32 bytes (one 16-column tile each); unit
-// u of row t is stored at u ^ f(t), f = (t & 3) | ((t >> 1) & 4), so the 8 rows
-// that 32 lanes read together (t = 0..3 and 8..11 of a half slab) fall on 64
-// distinct banks.
+// LDS rows are units of 32 bytes (one 16-column tile each); unit u of row t is
+// stored at u ^ f(t), f = (t & 3) | ((t >> 1) & 4), so the 8 rows that 32 lanes
+// read together (t = 0..3 and 8..11 of a half slab) fall on 64 distinct banks.
 // Rows past the segment's end read as zeros (buffer range check).
+//
+// Workgroups are persistent (one per CU, tiles w, w + G, ...) and their waves
+// have one role each.  Four copy waves keep a ring of three slabs filled across
+// tile boundaries.  The MFMA waves only read LDS, multiply and store: they wait
+// for no memory operation, so a tile's 4 BM BN bytes of output, which take about
+// as long to drain as a tile of 512 rows to multiply, leave under the next tiles.
+// (With every wave copying, a wave's copies wait behind its stores: 32 experts of
+// 4096 x 7168 with 512 rows each took 1.59 ms.)
+// Barrier u says that slab u has landed and that slab u - 1 has been read; the
+// copy waves then refill the stage of slab u - 1 with slab u + 2, and the MFMA
+// waves pass it in the last groups of slab u - 1, reading the first fragments
+// of slab u under the MFMAs that are left.
 
 #include "common.h"
 #include "launch.h"
@@ -35,131 +46,256 @@ struct RaggedWgradArgs {
   const uint16_t* x;
   int64_t ldx;
   const int32_t* seg;
-  int64_t total_rows, m, n;
+  int64_t num_experts, total_rows, m, n;
   float* c;
   int64_t tiles_m, tiles_n;
   int accumulate;
 };
 
-constexpr int kT = 64;                         // rows of a slab
+constexpr int kT = 64;                         // rows of a slab: two MFMAs' contraction
+constexpr int kRing = 3;
+constexpr int kBand = 4;                       // tile rows of a band: tiles walk down it, so the strips of dy
+                                               // and x that are read at a time stay few
 
 __device__ __forceinline__ int tswz(int t) { return (t & 3) | ((t >> 1) & 4); }
 
-struct WgStage {
-  uint8_t a[kT * 256];
-  uint8_t b[kT * 256];
-};
-template <int IDX>
-__device__ __forceinline__ WgStage& wg_stage() {
-  __shared__ __attribute__((aligned(16))) WgStage st;
-  return st;
-}
-
-__global__ __launch_bounds__(256) void ragged_wgrad_kernel(RaggedWgradArgs p) {
+template <int BM, int BN, bool STREAM>
+__global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_kernel(RaggedWgradArgs p) {
+  constexpr int WAVES_N = BN / 64, MW = BM / 64 * WAVES_N, TM = 4, TN = 4;      // 64 x 64 patches
+  constexpr int kSlabA = kT * BM * 2, kSlab = kSlabA + kT * BN * 2;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing * kSlab];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
   const int l16 = lane & 15, g = lane >> 4;
-
-  const int64_t tiles = p.tiles_m * p.tiles_n;
-  const int64_t e = (int64_t)blockIdx.x / tiles, tb = (int64_t)blockIdx.x - e * tiles;
-  const int64_t m0 = tb / p.tiles_n * 128, n0 = tb % p.tiles_n * 128;
+  const uint32_t tiles_m = (uint32_t)p.tiles_m, tiles_n = (uint32_t)p.tiles_n, tiles = tiles_m * tiles_n;
+  const uint32_t total = tiles * (uint32_t)p.num_experts, G = gridDim.x;
   const int cap = (int)p.total_rows;
-  const int s0 = min(max(p.seg[e], 0), cap);
-  const int rows = max(0, min(max(p.seg[e + 1], 0), cap) - s0);
-  if (rows == 0 && p.accumulate) return;
-  const int slabs = (rows + kT - 1) / kT;
+  // Workgroups are dealt to the 8 XCDs in turn; each round of G tiles gives every
+  // XCD a run of G / 8 consecutive ones, a block of kBand tile rows whose strips
+  // of dy and x its L2 holds.
+  const uint32_t first = G % 8 == 0 ? blockIdx.x % 8 * (G / 8) + blockIdx.x / 8 : blockIdx.x;
 
-  const uint16_t* const a0 = p.dy + (int64_t)s0 * p.ldy + m0;
-  const uint16_t* const b0 = p.x + (int64_t)s0 * p.ldx + n0;
-  const int64_t mw = min((int64_t)128, p.m - m0), nw = min((int64_t)128, p.n - n0);
-
-  // one copy instruction fills 4 rows; lane: row r4, stored chunk pc of 16
-  const int r4 = lane >> 4, pc = lane & 15;
-  auto issue = [&](int s, WgStage& st) {
-    const int64_t t0 = (int64_t)s * kT;
-    const int64_t left = rows - t0;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a0 + t0 * p.ldy, ((left - 1) * p.ldy + mw) * 2);
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(b0 + t0 * p.ldx, ((left - 1) * p.ldx + nw) * 2);
-#pragma unroll
-    for (int i = 0; i < kT / 16; ++i) {
-      const int q = wave + 4 * i, t = 4 * q + r4;
-      const int chunk = (((pc >> 1) ^ tswz(t)) << 1) | (pc & 1);
-      dma16(ra, st.a + q * 1024, (uint32_t)((int64_t)t * p.ldy * 2 + chunk * 16), 0);
-      dma16(rb, st.b + q * 1024, (uint32_t)((int64_t)t * p.ldx * 2 + chunk * 16), 0);
-    }
+  struct Tile {
+    uint32_t i, e;                             // i >= total: none
+    int64_t m0, n0;
+    int s0, rows, slabs;
   };
-  auto frag = [&](const uint8_t* base, int k0, int tile) -> v8bf {
-    v4i16 h[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int t = k0 + 8 * g + 4 * u + (l16 >> 2);
-      h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) v4i16*)(base + t * 256 + ((tile ^ tswz(t)) << 5) + ((l16 & 3) << 3)));
-    }
-    typedef short v8i16 __attribute__((ext_vector_type(8)));
-    const v8i16 r = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
-    return __builtin_bit_cast(v8bf, r);
+  auto tile_at = [&](uint32_t i) {
+    Tile t;
+    t.i = i;
+    t.e = i / tiles;
+    const uint32_t idx = i - t.e * tiles;
+    const uint32_t band = idx / (kBand * tiles_n), r = idx - band * kBand * tiles_n;
+    const uint32_t height = min((uint32_t)kBand, tiles_m - band * kBand);
+    t.m0 = (int64_t)(band * kBand + r % height) * BM;
+    t.n0 = (int64_t)(r / height) * BN;
+    t.s0 = min(max(p.seg[t.e], 0), cap);
+    t.rows = max(0, min(max(p.seg[t.e + 1], 0), cap) - t.s0);
+    t.slabs = (t.rows + kT - 1) / kT;
+    return t;
   };
-
-  v4f acc[4][4];                               // [n tile][m tile]
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
+  // the first tile from i on that has rows
+  auto live_tile = [&](uint32_t i) {
+    Tile t;
+    t.i = i;
+    t.slabs = 0;
+    for (; i < total; i += G) {
+      t = tile_at(i);
+      if (t.slabs > 0) return t;
+    }
+    t.i = total;
+    return t;
+  };
   auto barrier = [&]() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  auto slab = [&](int s, WgStage& cur, WgStage& nxt) {
-    if (s + 1 < slabs) {
-      issue(s + 1, nxt);
-      wait_vmcnt<2 * (kT / 16)>();             // this slab's copies have landed, the next one's may fly
-    } else {
-      wait_vmcnt<0>();
+
+  if (wave >= MW) {
+    // ======================= copy waves ==========================================
+    // A copy fills 1 KB: 2 (BM = 256) or 4 rows.  This wave copies q = c + 4i of a
+    // slab's; a row's swizzle depends on i only through t's bit 3.
+    const int c = wave - MW;
+    constexpr int A_CP = kSlabA / 4096, B_CP = kT * BN * 2 / 4096, kCopies = A_CP + B_CP;
+    auto lane_off = [&](int width, int64_t ld, int i) -> uint32_t {
+      const int chunks = width / 8, t = (c + 4 * i) * (64 / chunks) + lane / chunks, pc = lane % chunks;
+      return (uint32_t)((int64_t)(lane / chunks) * ld * 2 + (((((pc >> 1) ^ tswz(t)) << 1) | (pc & 1)) << 4));
+    };
+    const uint32_t off_a[2] = {lane_off(BM, p.ldy, 0), lane_off(BM, p.ldy, 1)};
+    const uint32_t off_b[2] = {lane_off(BN, p.ldx, 0), lane_off(BN, p.ldx, 1)};
+    auto issue = [&](const Tile& t, int s, int stage) {
+      const int64_t t0 = (int64_t)s * kT, left = t.rows - t0;
+      const int64_t mw = min((int64_t)BM, p.m - t.m0), nw = min((int64_t)BN, p.n - t.n0);
+      const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.dy + (t.s0 + t0) * p.ldy + t.m0, ((left - 1) * p.ldy + mw) * 2);
+      const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.x + (t.s0 + t0) * p.ldx + t.n0, ((left - 1) * p.ldx + nw) * 2);
+      uint8_t* const dst = lds + stage * kSlab;
+#pragma unroll
+      for (int i = 0; i < A_CP; ++i) {
+        const int q = c + 4 * i;
+        dma16(ra, dst + q * 1024, off_a[i & 1], (uint32_t)(q * (512 / BM)) * (uint32_t)(p.ldy * 2));
+      }
+#pragma unroll
+      for (int i = 0; i < B_CP; ++i) {
+        const int q = c + 4 * i;
+        dma16(rb, dst + kSlabA + q * 1024, off_b[i & 1], (uint32_t)(q * (512 / BN)) * (uint32_t)(p.ldx * 2));
+      }
+    };
+    Tile t = live_tile(first);
+    int s = 0, stage = 0, ahead = 0;           // the next slab to issue; slabs issued and not yet published
+    auto issue_next = [&]() {
+      if (t.i >= total) return;
+      issue(t, s, stage);
+      stage = stage == kRing - 1 ? 0 : stage + 1;
+      ++ahead;
+      if (++s == t.slabs) {
+        t = live_tile(t.i + G);
+        s = 0;
+      }
+    };
+    issue_next();
+    issue_next();
+    while (ahead > 0) {
+      if (ahead == 2) wait_vmcnt<kCopies>();
+      else wait_vmcnt<0>();
+      barrier();
+      --ahead;
+      issue_next();
     }
-    barrier();
-#pragma unroll
-    for (int k0 = 0; k0 < kT; k0 += 32) {
-      v8bf af[4], bf[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) af[j] = frag(cur.a, k0, 4 * wm + j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bf[i] = frag(cur.b, k0, 4 * wn + i);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[i], af[j], acc[i][j], 0, 0, 0);
-    }
-    __builtin_amdgcn_s_waitcnt(0xC07F);        // lgkmcnt(0): the slab is read before it is refilled
-    barrier();
-  };
-  if (slabs > 0) issue(0, wg_stage<0>());
-  for (int s = 0; s < slabs; s += 2) {
-    slab(s, wg_stage<0>(), wg_stage<1>());
-    if (s + 1 < slabs) slab(s + 1, wg_stage<1>(), wg_stage<0>());
+    return;
   }
 
-  float* const ce = p.c + e * p.m * p.n;
+  // ========================= MFMA waves ==========================================
+  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  // LDS offsets of the lane's words in slab 0: tile j of the wave's four, first
+  // read of k step 0; the second read lies 4 rows on, k step 1 32 rows on
+  const int tl = 8 * g + (l16 >> 2);
+  uint32_t at_a[TM], at_b[TN];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t*)lds;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int64_t row = m0 + 64 * wm + 16 * j + l16;
-    if (row >= p.m) continue;
+    at_a[j] = lds0 + (uint32_t)(tl * BM * 2 + (((TM * wm + j) ^ tswz(tl)) << 5) + ((l16 & 3) << 3));
+    at_b[j] = lds0 + (uint32_t)(kSlabA + tl * BN * 2 + (((TN * wn + j) ^ tswz(tl)) << 5) + ((l16 & 3) << 3));
+  }
+  auto frag = [&](uint32_t at, int row_bytes, int step) -> v8bf {
+    v4i16 h[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t col = n0 + 64 * wn + 16 * i + 4 * g;
-      if (col >= p.n) continue;
-      float* dst = ce + row * p.n + col;
-      float4 o = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-      if (p.accumulate) {
-        const float4 old = *reinterpret_cast<const float4*>(dst);
-        o.x += old.x; o.y += old.y; o.z += old.z; o.w += old.w;
+    for (int u = 0; u < 2; ++u)
+      h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4i16*)(uintptr_t)(at + (uint32_t)((32 * step + 4 * u) * row_bytes)));
+    typedef short v8i16 __attribute__((ext_vector_type(8)));
+    const v8i16 f = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
+    return __builtin_bit_cast(v8bf, f);
+  };
+  auto frag_a = [&](uint32_t stage, int j, int step) { return frag(at_a[j] + stage, BM * 2, step); };
+  auto frag_b = [&](uint32_t stage, int k, int step) { return frag(at_b[k] + stage, BN * 2, step); };
+
+  v4f acc[TN][TM];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  clear();
+
+  // Groups of one A fragment and its four MFMAs; A fragments are read kAhead
+  // groups ahead of them.
+  constexpr int kGroups = 2 * TM, kAhead = 3;
+  v8bf bf[2][TN], af[kAhead + 1];
+  uint32_t stage = 0;                          // byte offset of the current slab's stage
+  auto slab = [&](bool more) {
+    const uint32_t next = stage == (kRing - 1) * kSlab ? 0 : stage + kSlab;
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const int step = q / TM, j = q % TM, n = q + kAhead;
+      if (q < TN) bf[1][q] = frag_b(stage, q, 1);
+      if (n < kGroups) {
+        af[n % (kAhead + 1)] = frag_a(stage, n % TM, n / TM);
+      } else if (more) {
+        if (n == kGroups) {
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slab has been read
+          barrier();
+#pragma unroll
+          for (int k = 0; k < TN; ++k) bf[0][k] = frag_b(next, k, 0);
+        }
+        af[n % (kAhead + 1)] = frag_a(next, n - kGroups, 0);
       }
-      *reinterpret_cast<float4*>(dst) = o;
+#pragma unroll
+      for (int k = 0; k < TN; ++k)
+        acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[step][k], af[q % (kAhead + 1)], acc[k][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    stage = next;
+  };
+  auto store = [&](const Tile& t) {
+    const __amdgpu_buffer_rsrc_t rc =
+        make_rsrc(p.c + (int64_t)t.e * p.m * p.n + t.m0 * p.n, min((int64_t)BM, p.m - t.m0) * p.n * 4);
+    const bool hi = l16 >= 8;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+#pragma unroll
+      for (int k = 0; k < TN; k += 2) {
+        // lanes 8 apart swap one tile's piece for the other's, so that a store
+        // writes whole 128-byte lines (8 rows of 32 columns)
+        v4f o[2];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float send = hi ? acc[k][j][v] : acc[k + 1][j][v];
+          const float got = __uint_as_float(dpp_shuffle<0x128>(__float_as_uint(send)));
+          o[0][v] = hi ? got : acc[k][j][v];
+          o[1][v] = hi ? acc[k + 1][j][v] : got;
+        }
+        const int row = 64 * wm + 16 * j + (l16 & 7);
+        const int64_t col = t.n0 + 64 * wn + 16 * k + (hi ? 16 : 0) + 4 * g;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // rows past m end behind the range, columns past n are sent there
+          const uint32_t off = col < p.n ? (uint32_t)(((int64_t)(row + 8 * h) * p.n + col) * 4) : 0xFFFFFFF0u;
+          if (p.accumulate) {
+            const v4f old = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off, 0, 0));
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[h][v] += old[v];
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[h]), rc, (int)off, 0, STREAM ? 2 : 0);
+        }
+      }
+    }
+  };
+
+  Tile live = live_tile(first);
+  if (live.i < total) {
+    barrier();                                 // slab 0 landed
+#pragma unroll
+    for (int k = 0; k < TN; ++k) bf[0][k] = frag_b(0, k, 0);
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) af[n] = frag_a(0, n, 0);
+  }
+  for (uint32_t i = first; i < total; i += G) {
+    if (i == live.i) {
+      const Tile t = live;
+      live = live_tile(i + G);
+      for (int s = 0; s < t.slabs; ++s) slab(s + 1 < t.slabs || live.i < total);
+      store(t);
+      clear();
+    } else if (!p.accumulate) {
+      store(tile_at(i));                       // no rows: zeros
     }
   }
+}
+
+template <int BM, int BN>
+static int launch_ragged_wgrad(RaggedWgradArgs a, int64_t cus, hipStream_t s) {
+  a.tiles_m = (a.m + BM - 1) / BM;
+  a.tiles_n = (a.n + BN - 1) / BN;
+  const int64_t total = a.num_experts * a.tiles_m * a.tiles_n;
+  if (total > kMaxGrid) return FP8BS_ERR_SHAPE;
+  const dim3 g((unsigned)(total < cus ? total : cus)), b(64 * (BM / 64 * (BN / 64) + 4));
+  if (a.num_experts * a.m * a.n * 4 > kStreamBytes)
+    hipLaunchKernelGGL((ragged_wgrad_kernel<BM, BN, true>), g, b, 0, s, a);
+  else
+    hipLaunchKernelGGL((ragged_wgrad_kernel<BM, BN, false>), g, b, 0, s, a);
+  return launch_status();
 }
 
 }  // namespace fp8bs
@@ -172,13 +308,10 @@ extern "C" int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const
   if (!seg_offsets || !c || (total_rows > 0 && (!dy || !x))) return FP8BS_ERR_NULL;
   if (accumulate != 0 && accumulate != 1) return FP8BS_ERR_FLAG;
   if (num_experts < 1 || num_experts > 65536 || total_rows < 0 || total_rows > 0x3FFFFFFFLL || m <= 0 || n <= 0 ||
-      m % 8 || n % 8 || ldy < m || ldx < n || ldy > (1 << 24) || ldx > (1 << 24))
+      m % 8 || n % 8 || ldy < m || ldx < n || ldy > (1 << 24) || ldx > (1 << 24) || n > (1 << 21))
     return FP8BS_ERR_SHAPE;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(c, 16) || !aligned(seg_offsets, 4) || ldy % 8 || ldx % 8)
     return FP8BS_ERR_ALIGN;
-  RaggedWgradArgs a{dy, ldy, x, ldx, seg_offsets, total_rows, m, n, c, (m + 127) / 128, (n + 127) / 128, accumulate};
-  const int64_t grid = num_experts * a.tiles_m * a.tiles_n;
-  if (grid > kMaxGrid) return FP8BS_ERR_SHAPE;
-  hipLaunchKernelGGL(ragged_wgrad_kernel, dim3((unsigned)grid), dim3(256), 0, (hipStream_t)stream, a);
-  return launch_status();
+  RaggedWgradArgs a{dy, ldy, x, ldx, seg_offsets, num_experts, total_rows, m, n, c, 0, 0, accumulate};
+  return launch_ragged_wgrad<256, 128>(a, cu_count(), (hipStream_t)stream);
 }
