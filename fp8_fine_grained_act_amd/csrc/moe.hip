@@ -65,11 +65,13 @@ constexpr int kMaxTopk = 64;               // a token's slots fit in one wave's 
 // serialize in the workgroup's one memory pipeline.
 constexpr int kRouteBatch = 16;
 
-template <int PAD>
+// PAD: the segments' multiple.  TOKENS: the row -> token entries are written here
+// too (few pairs: one launch instead of two).
+template <int PAD, bool TOKENS = false>
 __global__ __launch_bounds__(1024) void moe_route_kernel(const int32_t* __restrict__ ids, int64_t pairs,
                                                          int num_e, int32_t* __restrict__ seg,
                                                          int32_t* __restrict__ slot_rows,
-                                                         int32_t* __restrict__ row_token, int64_t cap) {
+                                                         int32_t* __restrict__ row_token, int64_t cap, int topk) {
   __shared__ int next_row[kRouteWaves][kRouteMaxExperts];
   __shared__ int seg_s[kRouteMaxExperts + 1];
   __shared__ int cnt_s[kRouteMaxExperts];
@@ -159,7 +161,11 @@ __global__ __launch_bounds__(1024) void moe_route_kernel(const int32_t* __restri
 #pragma unroll
     for (int st = 0; st < kRouteBatch; ++st) {
       const int64_t i = b0 + 64 * st + lane;
-      if (i < hi && ev[st] >= 0 && ev[st] < num_e) slot_rows[i] = next_row[w][ev[st]] + rv[st];
+      if (i < hi && ev[st] >= 0 && ev[st] < num_e) {
+        const int r = next_row[w][ev[st]] + rv[st];
+        slot_rows[i] = r;
+        if (TOKENS && r < cap) row_token[r] = (int)(i / topk);
+      }
     }
   }
 
@@ -177,6 +183,174 @@ __global__ __launch_bounds__(256) void moe_route_rows_kernel(const int32_t* __re
   const int r = slot_rows[i];
   if (r >= 0 && r < cap) row_token[r] = (int)(i / topk);
 }
+
+// ---------------------------------------------------------------------------
+// Many pairs without padding rows: the same stable counting sort over chunks of
+// kRouteChunk pairs, one workgroup each, in three launches (one workgroup alone
+// took 77 us for 131072 pairs over 256 experts, its one CU's LDS and memory
+// pipelines the bound):
+//   route_count_kernel  a chunk's count of every expert
+//   route_scan_kernel   one workgroup: segment starts, and every (chunk, expert)
+//                       run's first row
+//   route_place_kernel  each pair's rank in its chunk, rows and tokens
+// Between the launches chunk b's counts, then first rows, lie in its own part of
+// slot_rows, at [b * kRouteChunk, + num_e): route_place_kernel takes them into
+// LDS before it writes that part, and no other workgroup reads them then.  A
+// last, shorter chunk may have no room for them: route_scan_kernel counts it
+// itself, and its first rows are the segments' ends less its own counts.
+constexpr int kRouteChunk = 2048;
+constexpr int64_t kRouteOnePairs = 8192;   // up to here one workgroup and launch
+static_assert(kRouteChunk >= kRouteMaxExperts && kRouteChunk % (64 * kRouteWaves) == 0, "whole waves, room for the counts");
+
+__global__ __launch_bounds__(256) void route_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int num_e,
+                                                          int32_t* __restrict__ slot_rows) {
+  __shared__ int cnt[kRouteMaxExperts];
+  for (int e = threadIdx.x; e < num_e; e += 256) cnt[e] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * kRouteChunk;
+#pragma unroll
+  for (int j = 0; j < kRouteChunk / 256; ++j) {
+    const int64_t i = lo + 256 * j + threadIdx.x;
+    const int e = i < pairs ? ids[i] : -1;
+    if (e >= 0 && e < num_e) atomicAdd(&cnt[e], 1);      // sums only: their order does not matter
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < num_e; e += 256) slot_rows[lo + e] = cnt[e];
+}
+
+// Wave w sums experts 64 (w mod EG) .. + 63 over part w / EG of the whole chunks.
+__global__ __launch_bounds__(1024) void route_scan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int num_e,
+                                                          int32_t* __restrict__ slot_rows,
+                                                          int32_t* __restrict__ seg) {
+  __shared__ int part_s[kRouteWaves][kRouteMaxExperts];
+  __shared__ int last_s[kRouteMaxExperts];
+  __shared__ int wave_sum[kRouteWaves];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t full = pairs / kRouteChunk;
+  const int groups = (num_e + 63) / 64, parts = kRouteWaves / groups;
+  const int part = w / groups, e = 64 * (w % groups) + lane;
+  const bool mine = part < parts && e < num_e;
+  const int64_t per = (full + parts - 1) / parts;
+  const int64_t b0 = min(full, part * per), b1 = min(full, b0 + per);
+
+  if (tid < kRouteMaxExperts) last_s[tid] = 0;
+  __syncthreads();
+  for (int64_t i = full * kRouteChunk + tid; i < pairs; i += 1024) {
+    const int x = ids[i];
+    if (x >= 0 && x < num_e) atomicAdd(&last_s[x], 1);
+  }
+  if (mine) {
+    int sum = 0;
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; ++b) sum += slot_rows[b * kRouteChunk + e];
+    part_s[part][e] = sum;
+  }
+  __syncthreads();
+  int count = 0;
+  if (tid < num_e) {
+    count = last_s[tid];
+    for (int p = 0; p < parts; ++p) count += part_s[p][tid];
+  }
+  int incl = count;
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) wave_sum[w] = incl;
+  __syncthreads();
+  if (tid < num_e) {
+    int run = incl - count;
+    for (int v = 0; v < w; ++v) run += wave_sum[v];
+    seg[tid] = run;
+    if (tid == num_e - 1) seg[num_e] = run + count;
+    for (int p = 0; p < parts; ++p) {
+      const int c = part_s[p][tid];
+      part_s[p][tid] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  if (mine) {
+    int run = part_s[part][e];
+    for (int64_t b = b0; b < b1; b += 8) {
+      int c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) c[u] = b + u < b1 ? slot_rows[(b + u) * kRouteChunk + e] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (b + u < b1) slot_rows[(b + u) * kRouteChunk + e] = run;
+        run += c[u];
+      }
+    }
+  }
+}
+
+// Ranks as in moe_route_kernel, kept in registers.
+__global__ __launch_bounds__(1024) void route_place_kernel(const int32_t* __restrict__ ids, int64_t pairs, int num_e,
+                                                           int topk, const int32_t* __restrict__ seg,
+                                                           int32_t* __restrict__ slot_rows,
+                                                           int32_t* __restrict__ row_token, int64_t cap) {
+  __shared__ int next_row[kRouteWaves][kRouteMaxExperts];
+  __shared__ unsigned long long match[kRouteWaves][kRouteMaxExperts];
+  constexpr int kSteps = kRouteChunk / (64 * kRouteWaves);
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t lo = (int64_t)blockIdx.x * kRouteChunk;
+  const bool whole = lo + kRouteChunk <= pairs;
+  int ev[kSteps], rank[kSteps], first = 0;
+#pragma unroll
+  for (int st = 0; st < kSteps; ++st) {
+    const int64_t i = lo + (int64_t)(w * kSteps + st) * 64 + lane;
+    const int e = i < pairs ? ids[i] : -1;
+    ev[st] = e >= 0 && e < num_e ? e : -1;
+  }
+  if (tid < num_e) {
+    first = whole ? slot_rows[lo + tid] : seg[tid + 1];
+    for (int v = 0; v < kRouteWaves; ++v) {
+      next_row[v][tid] = 0;
+      match[v][tid] = 0;
+    }
+  }
+  const int64_t total = seg[num_e];
+  __syncthreads();
+  const uint64_t below = (1ull << lane) - 1ull;
+#pragma unroll
+  for (int st = 0; st < kSteps; ++st) {
+    const int e = ev[st];
+    if (e >= 0) atomicOr(&match[w][e], 1ull << lane);
+    if (e >= 0) {
+      const uint64_t same = match[w][e];
+      const int before = __popcll(same & below), base = next_row[w][e];
+      rank[st] = base + before;
+      if (before == 0) {
+        next_row[w][e] = base + __popcll(same);
+        match[w][e] = 0;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid < num_e) {
+    int own = 0;
+    if (!whole)
+      for (int v = 0; v < kRouteWaves; ++v) own += next_row[v][tid];
+    int run = first - own;
+    for (int v = 0; v < kRouteWaves; ++v) {
+      const int c = next_row[v][tid];
+      next_row[v][tid] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int st = 0; st < kSteps; ++st) {
+    const int64_t i = lo + (int64_t)(w * kSteps + st) * 64 + lane;
+    if (i >= pairs) continue;
+    const int r = ev[st] >= 0 ? next_row[w][ev[st]] + rank[st] : -1;
+    slot_rows[i] = r;
+    if (r >= 0 && r < cap) row_token[r] = (int)(i / topk);
+  }
+  for (int64_t r = total + (int64_t)blockIdx.x * 1024 + tid; r < cap; r += (int64_t)gridDim.x * 1024) row_token[r] = -1;
+}
+
 
 // ---------------------------------------------------------------------------
 // Dispatch payload.  Token blocks: 4 waves, TPW tokens per wave; 8 lanes per
@@ -395,7 +569,7 @@ extern "C" int fp8bs_moe_route(const int32_t* topk_ids, int64_t tokens, int64_t 
     return FP8BS_ERR_ALIGN;
   const int64_t pairs = tokens * topk;
   hipLaunchKernelGGL(moe_route_kernel<kGroup>, dim3(1), dim3(64 * kRouteWaves), 0, (hipStream_t)stream, topk_ids, pairs,
-                     (int)num_experts, seg_offsets, slot_rows, row_token, rows_cap);
+                     (int)num_experts, seg_offsets, slot_rows, row_token, rows_cap, (int)topk);
   if (pairs > 0)
     hipLaunchKernelGGL(moe_route_rows_kernel, dim3((unsigned)((pairs + 255) / 256)), dim3(256), 0,
                        (hipStream_t)stream, slot_rows, pairs, (int)topk, row_token, rows_cap);
@@ -412,11 +586,20 @@ extern "C" int fp8bs_moe_route_ragged(const int32_t* topk_ids, int64_t tokens, i
   if (rows_cap < pairs || rows_cap > 0x7FFFFFFFLL) return FP8BS_ERR_SHAPE;
   if (!aligned(topk_ids, 4) || !aligned(seg_offsets, 4) || !aligned(slot_rows, 4) || !aligned(row_token, 4))
     return FP8BS_ERR_ALIGN;
-  hipLaunchKernelGGL(moe_route_kernel<1>, dim3(1), dim3(64 * kRouteWaves), 0, (hipStream_t)stream, topk_ids, pairs,
-                     (int)num_experts, seg_offsets, slot_rows, row_token, rows_cap);
-  if (pairs > 0)
-    hipLaunchKernelGGL(moe_route_rows_kernel, dim3((unsigned)((pairs + 255) / 256)), dim3(256), 0,
-                       (hipStream_t)stream, slot_rows, pairs, (int)topk, row_token, rows_cap);
+  hipStream_t s = (hipStream_t)stream;
+  if (pairs <= kRouteOnePairs) {
+    hipLaunchKernelGGL((moe_route_kernel<1, true>), dim3(1), dim3(64 * kRouteWaves), 0, s, topk_ids, pairs,
+                       (int)num_experts, seg_offsets, slot_rows, row_token, rows_cap, (int)topk);
+    return launch_status();
+  }
+  const int64_t blocks = (pairs + kRouteChunk - 1) / kRouteChunk;
+  if (blocks > kMaxGrid) return FP8BS_ERR_SHAPE;
+  hipLaunchKernelGGL(route_count_kernel, dim3((unsigned)(pairs / kRouteChunk)), dim3(256), 0, s, topk_ids, pairs,
+                     (int)num_experts, slot_rows);
+  hipLaunchKernelGGL(route_scan_kernel, dim3(1), dim3(64 * kRouteWaves), 0, s, topk_ids, pairs, (int)num_experts,
+                     slot_rows, seg_offsets);
+  hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)blocks), dim3(64 * kRouteWaves), 0, s, topk_ids, pairs,
+                     (int)num_experts, (int)topk, seg_offsets, slot_rows, row_token, rows_cap);
   return launch_status();
 }
 

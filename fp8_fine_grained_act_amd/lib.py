@@ -473,13 +473,8 @@ def fp8bs_moe_combine(y, slot_rows, gates, out=None, stream=None):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: a torch.cuda.Stream object costs 2 us
-
-
-def _on_device(dev, *named):
-    """Checks that the given tensors (or None) are on CUDA/HIP device index `dev`."""
-    for t, nm in named:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{nm} must be on cuda:{dev}")
+_current_device = torch._C._cuda_getDevice
+_Tensor, _bf16, _f32, _u8, _i32 = torch.Tensor, torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
 def _call(fn, dev, stream, *args):
@@ -491,7 +486,7 @@ def _call(fn, dev, stream, *args):
         handle = stream.cuda_stream
     else:
         raise ValueError(f"the stream must belong to cuda:{dev}")
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -500,18 +495,35 @@ def _call(fn, dev, stream, *args):
         raise Fp8bsError(fn.__name__, status)
 
 
-def _matrix(t, dtype, rows, cols, name):
-    """Checks a [rows, cols] tensor with unit column stride; returns its row stride.
+def _refuse(t, dtype, dev, name, what):
+    _dev(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    raise ValueError(f"{name} must be {what}")
+
+
+def _device_of(t, name):
+    """Device index of the tensor that decides where the call runs."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA/HIP tensor")
+    return t.get_device()
+
+
+def _dense(t, dtype, dev, name):
+    """Address of a contiguous tensor of this type on device index `dev`."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        _refuse(t, dtype, dev, name, "contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t, rows, cols, dev, name):
+    """(address, row stride) of a bf16 [rows, cols] tensor with unit column stride.
 
     A single row's stride says nothing about it: it counts as the row's length."""
-    _dev(t, dtype, name)
-    if t.shape != (rows, cols) or (t.stride(1) != 1 and cols > 1):
-        raise ValueError(f"{name} must be [{rows}, {cols}] with unit column stride")
-    return t.stride(0) if rows > 1 else cols
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    if not (isinstance(t, _Tensor) and t.dtype is _bf16 and t.get_device() == dev and t.shape == (rows, cols)
+            and (t.stride(1) == 1 or cols == 1)):
+        _refuse(t, _bf16, dev, name, f"[{rows}, {cols}] with unit column stride")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
 
 
 def fp8bs_gemm_epilogue(qa, sa, qb, sb, b_layout=0, bias=None, act=FP8BS_ACT_NONE, residual=None, z=None, c=None,
@@ -520,39 +532,39 @@ def fp8bs_gemm_epilogue(qa, sa, qb, sb, b_layout=0, bias=None, act=FP8BS_ACT_NON
 
     bias f32 [n]; residual bf16 [m, n] (may be c itself); z bf16 [m, n], filled with
     the pre-activations A B + bias when given (for fp8bs_epilogue_backward)."""
-    _contig(qa, torch.uint8, "qa")
-    _contig(sa, torch.float32, "sa")
-    _contig(qb, torch.uint8, "qb")
-    _contig(sb, torch.float32, "sb")
+    dev = _device_of(qa, "qa")
+    pqa, psa = _dense(qa, _u8, dev, "qa"), _dense(sa, _f32, dev, "sa")
+    pqb, psb = _dense(qb, _u8, dev, "qb"), _dense(sb, _f32, dev, "sb")
+    if b_layout != 0 and b_layout != 1:
+        raise ValueError("b_layout must be 0 or 1")
     if qa.dim() != 2 or qb.dim() != 2:
         raise ValueError("qa and qb must be matrices")
-    if b_layout not in (0, 1):
-        raise ValueError("b_layout must be 0 or 1")
     m, k = qa.shape
-    n, kb = (qb.shape[0], qb.shape[1]) if b_layout == 0 else (qb.shape[1], qb.shape[0])
-    blocks = (qb.shape[0] // GROUP, qb.shape[1] // GROUP)
-    if kb != k or sa.shape != (m, k // GROUP) or sb.shape != blocks:
+    rows, cols = qb.shape
+    n = cols if b_layout else rows
+    if (rows if b_layout else cols) != k or sa.shape != (m, k // GROUP) or sb.shape != (rows // GROUP, cols // GROUP):
         raise ValueError("operand and scale shapes do not match")
     if c is None:
-        c = torch.empty((m, n), dtype=torch.bfloat16, device=qa.device)
-    ldc = _matrix(c, torch.bfloat16, m, n, "c")
-    ldr = _matrix(residual, torch.bfloat16, m, n, "residual") if residual is not None else 0
-    ldz = _matrix(z, torch.bfloat16, m, n, "z") if z is not None else 0
-    if bias is not None and _contig(bias, torch.float32, "bias").shape != (n,):
-        raise ValueError("bias must be [n]")
-    dev = qa.get_device()
-    _on_device(dev, (sa, "sa"), (qb, "qb"), (sb, "sb"), (bias, "bias"), (residual, "residual"), (z, "z"), (c, "c"))
-    _call(raw.fp8bs_gemm_epilogue, dev, stream, qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), m, n, k,
-          b_layout, _ptr(bias), act, _ptr(residual), ldr, _ptr(z), ldz, c.data_ptr(), ldc)
+        c = torch.empty((m, n), dtype=_bf16, device=qa.device)
+    pc, ldc = _matrix(c, m, n, dev, "c")
+    pr, ldr = (None, 0) if residual is None else _matrix(residual, m, n, dev, "residual")
+    pz, ldz = (None, 0) if z is None else _matrix(z, m, n, dev, "z")
+    pbias = None
+    if bias is not None:
+        pbias = _dense(bias, _f32, dev, "bias")
+        if bias.shape != (n,):
+            raise ValueError("bias must be [n]")
+    _call(raw.fp8bs_gemm_epilogue, dev, stream, pqa, psa, pqb, psb, m, n, k, b_layout, pbias, act, pr, ldr, pz, ldz,
+          pc, ldc)
     return c
 
 
 def fp8bs_epilogue_backward_workspace(m, n):
     """Bytes of workspace that fp8bs_epilogue_backward needs for dbias (host only)."""
-    r = raw.fp8bs_epilogue_backward_workspace(int(m), int(n))
+    r = raw.fp8bs_epilogue_backward_workspace(m, n)
     if r < 0:
         raise Fp8bsError("fp8bs_epilogue_backward_workspace", r)
-    return int(r)
+    return r
 
 
 def fp8bs_epilogue_backward(dy, z, act=FP8BS_ACT_NONE, dz=None, dbias=None, accumulate=0, workspace=None,
@@ -563,34 +575,43 @@ def fp8bs_epilogue_backward(dy, z, act=FP8BS_ACT_NONE, dz=None, dbias=None, accu
     or z), None to allocate one, or False to leave that result out.  workspace: a
     contiguous float32 tensor of at least fp8bs_epilogue_backward_workspace(m, n)
     bytes, or None to allocate one."""
-    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+    dev = _device_of(dy, "dy")
+    if dy.dim() != 2:
         raise ValueError("dy must be a bf16 matrix")
     m, n = dy.shape
-    ldy = _matrix(dy, torch.bfloat16, m, n, "dy")
-    ldz = 0
+    pdy, ldy = _matrix(dy, m, n, dev, "dy")
+    pz, ldz = None, 0
     if z is not None:
-        ldz = _matrix(z, torch.bfloat16, m, n, "z")
+        pz, ldz = _matrix(z, m, n, dev, "z")
     elif act != FP8BS_ACT_NONE:
         raise ValueError("z is needed for this activation")
-    if accumulate and not isinstance(dbias, torch.Tensor):
+    if accumulate and (dbias is None or dbias is False):
         raise ValueError("accumulate needs a dbias to add to")
-    dz = torch.empty((m, n), dtype=torch.bfloat16, device=dy.device) if dz is None else (None if dz is False else dz)
-    dbias = torch.empty(n, dtype=torch.float32, device=dy.device) if dbias is None else (None if dbias is False else dbias)
-    lddz = _matrix(dz, torch.bfloat16, m, n, "dz") if dz is not None else 0
-    if dbias is not None and _contig(dbias, torch.float32, "dbias").shape != (n,):
-        raise ValueError("dbias must be [n]")
-    if workspace is None and dbias is not None:
-        need = fp8bs_epilogue_backward_workspace(m, n)
-        if need:
-            workspace = torch.empty(need // 4, dtype=torch.float32, device=dy.device)
-            if stream is not None:
-                workspace.record_stream(stream)    # kept until that stream has used it
-    elif workspace is not None:
-        _contig(workspace, torch.float32, "workspace")
-    dev = dy.get_device()
-    _on_device(dev, (z, "z"), (dz, "dz"), (dbias, "dbias"), (workspace, "workspace"))
-    _call(raw.fp8bs_epilogue_backward, dev, stream, dy.data_ptr(), ldy, _ptr(z), ldz, m, n, act, _ptr(dz), lddz,
-          _ptr(dbias), accumulate, _ptr(workspace), 0 if workspace is None else 4 * workspace.numel())
+    pdz, lddz, pdb, pws, ws_bytes = None, 0, None, None, 0
+    if dz is False:
+        dz = None
+    else:
+        if dz is None:
+            dz = torch.empty((m, n), dtype=_bf16, device=dy.device)
+        pdz, lddz = _matrix(dz, m, n, dev, "dz")
+    if dbias is False:
+        dbias = None
+    else:
+        if dbias is None:
+            dbias = torch.empty(n, dtype=_f32, device=dy.device)
+        pdb = _dense(dbias, _f32, dev, "dbias")
+        if dbias.shape != (n,):
+            raise ValueError("dbias must be [n]")
+        if workspace is None:
+            need = fp8bs_epilogue_backward_workspace(m, n)
+            if need:
+                workspace = torch.empty(need // 4, dtype=_f32, device=dy.device)
+                if stream is not None:
+                    workspace.record_stream(stream)    # kept until that stream has used it
+    if workspace is not None:
+        pws, ws_bytes = _dense(workspace, _f32, dev, "workspace"), 4 * workspace.numel()
+    _call(raw.fp8bs_epilogue_backward, dev, stream, pdy, ldy, pz, ldz, m, n, act, pdz, lddz, pdb, accumulate, pws,
+          ws_bytes)
     return dz, dbias
 
 
@@ -599,28 +620,25 @@ def fp8bs_moe_route_ragged(topk_ids, num_experts, rows_cap=None, seg_offsets=Non
     """fp8bs_moe_route without padding rows: (seg_offsets [E+1], slot_rows [T, k], row_token [cap]).
 
     rows_cap (default: tokens * topk) must be at least tokens * topk."""
-    _contig(topk_ids, torch.int32, "topk_ids")
+    dev = _device_of(topk_ids, "topk_ids")
+    pids = _dense(topk_ids, _i32, dev, "topk_ids")
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be [tokens, topk]")
     tokens, topk = topk_ids.shape
     if rows_cap is None:
         rows_cap = tokens * topk
-    dev = topk_ids.device
+    on = topk_ids.device
     if seg_offsets is None:
-        seg_offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+        seg_offsets = torch.empty(num_experts + 1, dtype=_i32, device=on)
     if slot_rows is None:
-        slot_rows = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+        slot_rows = torch.empty((tokens, topk), dtype=_i32, device=on)
     if row_token is None:
-        row_token = torch.empty(rows_cap, dtype=torch.int32, device=dev)
-    outs = ((seg_offsets, "seg_offsets"), (slot_rows, "slot_rows"), (row_token, "row_token"))
-    for t, nm in outs:
-        _contig(t, torch.int32, nm)
-    if seg_offsets.numel() != num_experts + 1 or tuple(slot_rows.shape) != (tokens, topk) \
-            or row_token.numel() != rows_cap:
+        row_token = torch.empty(rows_cap, dtype=_i32, device=on)
+    pseg, pslot = _dense(seg_offsets, _i32, dev, "seg_offsets"), _dense(slot_rows, _i32, dev, "slot_rows")
+    ptok = _dense(row_token, _i32, dev, "row_token")
+    if seg_offsets.numel() != num_experts + 1 or slot_rows.shape != (tokens, topk) or row_token.numel() != rows_cap:
         raise ValueError("output shapes do not match the routing")
-    _on_device(topk_ids.get_device(), *outs)
-    _call(raw.fp8bs_moe_route_ragged, topk_ids.get_device(), stream, topk_ids.data_ptr(), tokens, topk, num_experts,
-          seg_offsets.data_ptr(), slot_rows.data_ptr(), row_token.data_ptr(), rows_cap)
+    _call(raw.fp8bs_moe_route_ragged, dev, stream, pids, tokens, topk, num_experts, pseg, pslot, ptok, rows_cap)
     return seg_offsets, slot_rows, row_token
 
 
@@ -630,30 +648,26 @@ def fp8bs_grouped_gemm_ragged(qa, sa, seg_offsets, qb, sb, b_layout=0, c=None, s
     qb [E, n, k] for b_layout 0, [E, k, n] for 1 (the forward weights as stored);
     seg_offsets int32 [E+1] on the device.  Rows of c outside every segment are left
     as they are."""
-    _contig(qa, torch.uint8, "qa")
-    _contig(sa, torch.float32, "sa")
-    _contig(qb, torch.uint8, "qb")
-    _contig(sb, torch.float32, "sb")
-    _contig(seg_offsets, torch.int32, "seg_offsets")
+    dev = _device_of(qa, "qa")
+    pqa, psa = _dense(qa, _u8, dev, "qa"), _dense(sa, _f32, dev, "sa")
+    pqb, psb = _dense(qb, _u8, dev, "qb"), _dense(sb, _f32, dev, "sb")
+    pseg = _dense(seg_offsets, _i32, dev, "seg_offsets")
+    if b_layout != 0 and b_layout != 1:
+        raise ValueError("b_layout must be 0 or 1")
     if qa.dim() != 2 or qb.dim() != 3:
         raise ValueError("qa must be [rows, k] and qb [experts, ., .]")
-    if b_layout not in (0, 1):
-        raise ValueError("b_layout must be 0 or 1")
     rows, k = qa.shape
-    num_e = qb.shape[0]
-    n, kb = (qb.shape[1], qb.shape[2]) if b_layout == 0 else (qb.shape[2], qb.shape[1])
-    blocks = (num_e, qb.shape[1] // GROUP, qb.shape[2] // GROUP)
-    if kb != k or sa.shape != (rows, k // GROUP) or sb.shape != blocks:
+    num_e, b_rows, b_cols = qb.shape
+    n = b_cols if b_layout else b_rows
+    if (b_rows if b_layout else b_cols) != k or sa.shape != (rows, k // GROUP) \
+            or sb.shape != (num_e, b_rows // GROUP, b_cols // GROUP):
         raise ValueError("operand and scale shapes do not match")
     if seg_offsets.numel() != num_e + 1:
         raise ValueError("seg_offsets must have num_experts + 1 entries")
     if c is None:
-        c = torch.empty((rows, n), dtype=torch.bfloat16, device=qa.device)
-    ldc = _matrix(c, torch.bfloat16, rows, n, "c")
-    dev = qa.get_device()
-    _on_device(dev, (sa, "sa"), (qb, "qb"), (sb, "sb"), (seg_offsets, "seg_offsets"), (c, "c"))
-    _call(raw.fp8bs_grouped_gemm_ragged, dev, stream, qa.data_ptr(), sa.data_ptr(),
-          seg_offsets.data_ptr(), num_e, rows, qb.data_ptr(), sb.data_ptr(), n, k, b_layout, c.data_ptr(), ldc)
+        c = torch.empty((rows, n), dtype=_bf16, device=qa.device)
+    pc, ldc = _matrix(c, rows, n, dev, "c")
+    _call(raw.fp8bs_grouped_gemm_ragged, dev, stream, pqa, psa, pseg, num_e, rows, pqb, psb, n, k, b_layout, pc, ldc)
     return c
 
 
@@ -661,22 +675,21 @@ def fp8bs_grouped_wgrad_ragged(dy, x, seg_offsets, c=None, accumulate=0, stream=
     """Experts' weight gradients f32 C [E, m, n]: C[e] (+)= dy_e^T x_e over the rows of segment e.
 
     dy bf16 [R, m], x bf16 [R, n]; seg_offsets int32 [E+1] on the device."""
-    if not isinstance(dy, torch.Tensor) or not isinstance(x, torch.Tensor) or dy.dim() != 2 or x.dim() != 2:
-        raise ValueError("dy and x must be bf16 matrices")
+    dev = _device_of(dy, "dy")
+    pseg = _dense(seg_offsets, _i32, dev, "seg_offsets")
+    if dy.dim() != 2 or not isinstance(x, _Tensor) or x.dim() != 2 or seg_offsets.numel() < 1:
+        raise ValueError("dy and x must be bf16 matrices and seg_offsets [experts + 1]")
     rows, m = dy.shape
     n = x.shape[1]
-    ldy = _matrix(dy, torch.bfloat16, rows, m, "dy")
-    ldx = _matrix(x, torch.bfloat16, rows, n, "x")
-    _contig(seg_offsets, torch.int32, "seg_offsets")
+    pdy, ldy = _matrix(dy, rows, m, dev, "dy")
+    px, ldx = _matrix(x, rows, n, dev, "x")
     num_e = seg_offsets.numel() - 1
-    if accumulate and c is None:
-        raise ValueError("accumulate needs a c to add to")
     if c is None:
-        c = torch.empty((max(num_e, 0), m, n), dtype=torch.float32, device=dy.device)
-    if _contig(c, torch.float32, "c").shape != (num_e, m, n):
+        if accumulate:
+            raise ValueError("accumulate needs a c to add to")
+        c = torch.empty((num_e, m, n), dtype=_f32, device=dy.device)
+    pc = _dense(c, _f32, dev, "c")
+    if c.shape != (num_e, m, n):
         raise ValueError("c must be [experts, m, n]")
-    dev = dy.get_device()
-    _on_device(dev, (x, "x"), (seg_offsets, "seg_offsets"), (c, "c"))
-    _call(raw.fp8bs_grouped_wgrad_ragged, dev, stream, dy.data_ptr(), ldy, x.data_ptr(), ldx,
-          seg_offsets.data_ptr(), num_e, rows, m, n, c.data_ptr(), accumulate)
+    _call(raw.fp8bs_grouped_wgrad_ragged, dev, stream, pdy, ldy, px, ldx, pseg, num_e, rows, m, n, pc, accumulate)
     return c
