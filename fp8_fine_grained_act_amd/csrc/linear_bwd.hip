@@ -3,21 +3,28 @@
 //   dz[i, j] = dy[i, j] * act'(z[i, j]),   dbias[j] (+)= sum_i dz[i, j]
 //
 // (the residual's gradient is dy itself).  dz goes on to the quantizers and the
-// dgrad and wgrad products.  One pass over dy and z: a workgroup of kWaves waves
-// owns a strip of 64 x VEC columns and a run of rows, wave w taking rows w,
-// w + kWaves, ...; each lane sums its VEC columns' FP32 dz in registers, the
-// waves' sums meet in LDS in wave order.  With one run of rows the workgroup
-// writes dbias itself; otherwise its sums go to the caller's workspace
-// [runs][n] and bias_sum_kernel adds the runs in order.  No atomics: the bits
-// depend on (m, n) only.  dbias sums the FP32 dz, before its bf16 rounding.
+// dgrad and wgrad products.  One pass over dy and z, bound by HBM (6 bytes per
+// element): a workgroup owns a strip of 512 columns and a run of rows, wave w
+// taking rows w, w + kBwdWaves, ...; each lane sums its 8 columns' FP32 dz in
+// registers, the waves' sums meet in LDS in wave order.  With one run of rows
+// the workgroup writes dbias itself; otherwise its sums go to the caller's
+// workspace [runs][n] and bias_sum_kernel adds the runs in order.  No atomics:
+// the bits depend on (m, n) only.  dbias sums the FP32 dz, before its bf16
+// rounding.
+//
+// About 512 workgroups of 8 waves with 2 rows each in flight: 16384 x 4096 with
+// GELU in 75 us, both launches (403 MB, 5.4 TB/s).  2048 workgroups of 4 waves with 4
+// rows each took 107 us, 1024 of them 89 us, 256 of 8 waves 76 us; without the
+// non-temporal hint the shipped form takes 82 us (4096 x 4096, which the
+// last-level cache holds, 23.8 us without and 27 us with it).
 
 #include "common.h"
 #include "launch.h"
 
 namespace fp8bs {
 
-constexpr int kBwdWaves = 4;
-constexpr int kBwdUnroll = 4;                  // rows of a wave in flight
+constexpr int kBwdWaves = 8;
+constexpr int kBwdUnroll = 2;                  // rows of a wave in flight
 
 struct BwdArgs {
   const uint16_t* dy;
@@ -31,7 +38,9 @@ struct BwdArgs {
   int accumulate;                              // one run: add to sums
 };
 
-template <int ACT>
+// STREAM: the call's bytes are larger than half the last-level cache, and pass
+// through with the non-temporal hint.
+template <int ACT, bool STREAM>
 __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p) {
   __shared__ float part[kBwdWaves][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -39,6 +48,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
   const bool live = col < p.n;
   const int64_t r0 = (int64_t)blockIdx.y * p.run_rows;
   const int64_t r1 = min(p.m, r0 + p.run_rows);
+  auto load = [](const uint16_t* a) { return STREAM ? load_nt(a) : *reinterpret_cast<const uint4*>(a); };
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
@@ -51,8 +61,8 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
         const int64_t row = r + u * kBwdWaves;
         d[u] = zv[u] = make_uint4(0, 0, 0, 0);
         if (row < r1) {
-          d[u] = *reinterpret_cast<const uint4*>(p.dy + row * p.ldy + col);
-          if (ACT != FP8BS_ACT_NONE) zv[u] = *reinterpret_cast<const uint4*>(p.z + row * p.ldz + col);
+          d[u] = load(p.dy + row * p.ldy + col);
+          if (ACT != FP8BS_ACT_NONE) zv[u] = load(p.z + row * p.ldz + col);
         }
       }
 #pragma unroll
@@ -70,7 +80,10 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
           sum[2 * i + 1] += hi;
           o[i] = f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
         }
-        if (p.dz) *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (!p.dz) continue;
+        uint16_t* const dst = p.dz + row * p.lddz + col;
+        if (STREAM) store_nt(dst, make_uint4(o[0], o[1], o[2], o[3]));
+        else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -108,10 +121,10 @@ __global__ __launch_bounds__(1024) void bias_sum_kernel(const float* __restrict_
   }
 }
 
-// Rows per run: about 2048 workgroups over the strips, 32 rows or more each.
+// Rows per run: about 512 workgroups over the strips, 64 rows or more each.
 static int64_t bwd_run_rows(int64_t m, int64_t n) {
   const int64_t strips = (n + 511) / 512;
-  const int64_t want = strips < 2048 ? 2048 / strips : 1;
+  const int64_t want = strips < 512 ? 512 / strips : 1;
   int64_t rows = (m + want - 1) / want;
   rows = (rows + 15) / 16 * 16;
   if (rows < 64) rows = 64;
@@ -119,6 +132,15 @@ static int64_t bwd_run_rows(int64_t m, int64_t n) {
   return rows < least ? least : rows;
 }
 static int64_t bwd_runs(int64_t m, int64_t n) { return (m + bwd_run_rows(m, n) - 1) / bwd_run_rows(m, n); }
+
+template <int ACT>
+static void launch_bwd(const BwdArgs& a, int64_t runs, hipStream_t s) {
+  const dim3 grid((unsigned)((a.n + 511) / 512), (unsigned)runs), block(64 * kBwdWaves);
+  if (6 * a.m * a.n > kStreamBytes)
+    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, false>), grid, block, 0, s, a);
+}
 
 }  // namespace fp8bs
 
@@ -147,13 +169,12 @@ extern "C" int fp8bs_epilogue_backward(const uint16_t* dy, int64_t ldy, const ui
   const bool two = dbias && runs > 1;
   if (two && (!workspace || workspace_bytes < fp8bs_epilogue_backward_workspace(m, n))) return FP8BS_ERR_SCRATCH;
   BwdArgs a{dy, ldy, z, ldz, dz, lddz, two ? workspace : dbias, m, n, rows, two ? 0 : accumulate};
-  const dim3 grid((unsigned)((n + 511) / 512), (unsigned)runs), block(64 * kBwdWaves);
   hipStream_t s = (hipStream_t)stream;
   switch (act) {
-    case FP8BS_ACT_RELU: hipLaunchKernelGGL(epilogue_bwd_kernel<FP8BS_ACT_RELU>, grid, block, 0, s, a); break;
-    case FP8BS_ACT_GELU_TANH: hipLaunchKernelGGL(epilogue_bwd_kernel<FP8BS_ACT_GELU_TANH>, grid, block, 0, s, a); break;
-    case FP8BS_ACT_SILU: hipLaunchKernelGGL(epilogue_bwd_kernel<FP8BS_ACT_SILU>, grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL(epilogue_bwd_kernel<FP8BS_ACT_NONE>, grid, block, 0, s, a); break;
+    case FP8BS_ACT_RELU: launch_bwd<FP8BS_ACT_RELU>(a, runs, s); break;
+    case FP8BS_ACT_GELU_TANH: launch_bwd<FP8BS_ACT_GELU_TANH>(a, runs, s); break;
+    case FP8BS_ACT_SILU: launch_bwd<FP8BS_ACT_SILU>(a, runs, s); break;
+    default: launch_bwd<FP8BS_ACT_NONE>(a, runs, s); break;
   }
   if (two)
     hipLaunchKernelGGL(bias_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, s, workspace, runs, n, dbias,
