@@ -909,6 +909,11 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   Stage<BM, BN>& st0 = lds_stage<BM, BN, 0>();
   Stage<BM, BN>& st1 = lds_stage<BM, BN, 1>();
   Stage<BM, BN>& st2 = lds_stage<BM, BN, 2>();
+  // ragged: the A row scales of four slabs at a time, [group of slabs & 1][row][4].
+  // One slab's scales lie nkb * 4 bytes apart, a request to the L2 for every
+  // row, which took a third of the copies' requests; four neighbours of a row
+  // share one (256 experts of 4096 x 7168 with 128 rows each: 1.94 -> 1.7 ms).
+  __shared__ float sa4[2][VAR == kRagged ? 4 * BM : 1];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -1039,7 +1044,12 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     // scale jobs: wave c < SA_JOBS copies A rows 64c .. 64c+63, wave
     // c < SB_JOBS also B columns 64c .. 64c+63 (voff_sb, set per tile)
     const uint32_t voff_sa = (uint32_t)((64 * c + lane) * nkb) * 4u;
-    const int my_jobs = A_CP + B_CP + (c < SA_JOBS ? 1 : 0) + (c < SB_JOBS ? 1 : 0);
+    // ragged: copy q = c + 4i covers 16 rows, 4 slabs' scales each (past the
+    // last slab: scales of the next row, not used)
+    const uint32_t voff_sa4 = (uint32_t)((16 * c + (lane >> 2)) * nkb + (lane & 3)) * 4u;
+    auto jobs = [&](int kb) {
+      return A_CP + B_CP + (VAR == kRagged ? (kb % 4 == 0 ? BM / 64 : 0) : (c < SA_JOBS ? 1 : 0)) + (c < SB_JOBS ? 1 : 0);
+    };
     auto issue = [&](int kb, Stage<BM, BN>& s) {
       const uint32_t ks = (uint32_t)kb * BK;
 #pragma unroll
@@ -1052,7 +1062,15 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
         else
           dma16(rb, s.b + (c + 4 * i) * 1024, voff_b, ks + (uint32_t)(32 * i) * (uint32_t)K);
       }
-      if (c < SA_JOBS) dma4(rsa, s.sa + 64 * c, voff_sa, (uint32_t)kb * 4u);
+      if (VAR == kRagged) {
+        if (kb % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < BM / 64; ++i)
+            dma4(rsa, &sa4[(kb >> 2) & 1][64 * (c + 4 * i)], voff_sa4, (uint32_t)(64 * i * nkb + kb) * 4u);
+        }
+      } else if (c < SA_JOBS) {
+        dma4(rsa, s.sa + 64 * c, voff_sa, (uint32_t)kb * 4u);
+      }
       if (c < SB_JOBS) {
         if (MODE == kDgrad)
           dma4(rsb, s.sb + 64 * c, voff_sb, (uint32_t)kb * (uint32_t)(N / 128) * 4u);
@@ -1079,7 +1097,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     issue_next(st0);
     if (units > 1) {
       issue_next(st1);
-      wait_vmcnt_dyn(my_jobs);
+      wait_vmcnt_dyn(jobs(kb0 + ikb - 1));
     } else {
       wait_vmcnt<0>();
     }
@@ -1088,11 +1106,11 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     // per unit (in its last group), else one per unit (at its start); the
     // copy waves pass the prologue barrier plus one per phase, except the
     // last phase in the second case
-    constexpr bool kEarly = MODE != kDgrad;
+    constexpr bool kEarly = MODE != kDgrad && VAR != kRagged;
     auto phase = [&](int u, Stage<BM, BN>& fill) {
       if (u + 2 < units) {
         issue_next(fill);
-        wait_vmcnt_dyn(my_jobs);                                    // unit u + 1 landed
+        wait_vmcnt_dyn(jobs(kb0 + ikb - 1));                                    // unit u + 1 landed
       } else {
         wait_vmcnt<0>();
       }
@@ -1108,15 +1126,21 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
 
   // ========================= MFMA waves ==========================================
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
-  const int ra0 = WM * wm + l16, rb0 = WN * wn + l16;
+  // A wave's 16-row groups: consecutive, or, for ragged segments, dealt to the
+  // waves in turn, so that a tile with fewer rows leaves every wave fewer
+  // groups (the slab loop then runs only those: see run_groups)
+  constexpr int kGroupRows = VAR == kRagged ? 16 * WAVES_M : 16;
+  const int wrow = VAR == kRagged ? 16 * wm : WM * wm;
+  const int ra0 = wrow + l16, rb0 = WN * wn + l16;
   // rows ra0 + 16t share ra0's swizzle, so tile t adds 16t rows
   const int a_lo = swz(ra0, 2 * g), a_hi = swz(ra0, 2 * g + 1);
   const int b_lo = swz(rb0, 2 * g), b_hi = swz(rb0, 2 * g + 1);
-  auto frag = [&](const uint8_t* base, int lo, int hi, int t) -> v8i {
-    const uint4 x = *reinterpret_cast<const uint4*>(base + lo + t * 16 * BK);
-    const uint4 y = *reinterpret_cast<const uint4*>(base + hi + t * 16 * BK);
+  auto frag = [&](const uint8_t* base, int lo, int hi, int t, int step = 16) -> v8i {
+    const uint4 x = *reinterpret_cast<const uint4*>(base + lo + t * step * BK);
+    const uint4 y = *reinterpret_cast<const uint4*>(base + hi + t * step * BK);
     return v8i{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
   };
+  auto frag_a = [&](const uint8_t* base, int t) -> v8i { return frag(base, a_lo, a_hi, t, kGroupRows); };
   // dgrad: rows of the B slab are k; lane (g, l16) gathers k = 32g .. 32g+31 of
   // column WN*wn + 16i + l16 with ds_read_b64_tr_b8
   auto frag_b_tr = [&](const uint8_t* base, int i) -> v8i {
@@ -1159,13 +1183,18 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   };
   // reads in the order of first use: B fragment 0 and A fragment 0 (the
   // first MFMA), the scales (its fold), then the other B fragments
-  auto read_head = [&](const Stage<BM, BN>& s) {
+  // row scales of this wave's rows in slab kb: ra0's, then one every kScaleStep
+  constexpr int kScaleStep = (VAR == kRagged ? 4 : 1) * kGroupRows;
+  auto row_scales = [&](const Stage<BM, BN>& s, int kb) -> const float* {
+    return VAR == kRagged ? &sa4[(kb >> 2) & 1][4 * ra0 + (kb & 3)] : &s.sa[ra0];
+  };
+  auto read_head = [&](const Stage<BM, BN>& s, const float* sap) {
     Head h;
     h.bf[0] = MODE == kDgrad ? frag_b_tr(s.b, 0) : frag(s.b, b_lo, b_hi, 0);
-    h.a0 = frag(s.a, a_lo, a_hi, 0);
-    h.wa0 = s.sa[WM * wm + l16];
-    h.a1 = frag(s.a, a_lo, a_hi, TM > 1 ? 1 : 0);
-    h.wa1 = s.sa[WM * wm + (TM > 1 ? 16 : 0) + l16];
+    h.a0 = frag_a(s.a, 0);
+    h.wa0 = sap[0];
+    h.a1 = frag_a(s.a, TM > 1 ? 1 : 0);
+    h.wa1 = sap[TM > 1 ? kScaleStep : 0];
     if (MODE == kWgrad) {
 #pragma unroll
       for (int i = 0; i < TN; ++i) h.wb[i] = *reinterpret_cast<const v4f*>(&s.sb[WN * wn + 16 * i + 4 * g]);
@@ -1217,12 +1246,12 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // MFMAs.  dgrad keeps the barrier at the start of each slab: its head is
   // 16 transposing LDS reads, more than one group's MFMAs hide, and it
   // measured 7% slower with the early head.
-  constexpr bool kEarly = MODE != kDgrad;
+  constexpr bool kEarly = MODE != kDgrad && VAR != kRagged;
   if (W16) barrier();                          // the copy waves' exchange of slab 0's block maxima
   Head hd;
   if (kEarly) {
     barrier();                                 // slab 0 landed
-    hd = read_head(st0);
+    hd = read_head(st0, row_scales(st0, 0));
   }
 
   // Slab kb from stage s; the last group passes barrier kb + 1 (every LDS read
@@ -1230,31 +1259,33 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // and reads the head of slab kb + 1 from stage sn (A fragments and scales
   // first, then each B fragment after its last MFMA here).  After the final
   // slab that head is never used.
-  auto slab = [&](const Stage<BM, BN>& s, const Stage<BM, BN>& sn) {
+  auto slab = [&](auto groups, int kb, const Stage<BM, BN>& s, const Stage<BM, BN>& sn) __attribute__((always_inline)) {
+    constexpr int GR = decltype(groups)::value;               // 16-row groups multiplied
+    const float* const sap = row_scales(s, kb);
     if (!kEarly) {
       barrier();
-      hd = read_head(s);
+      hd = read_head(s, sap);
     }
     v8i a_cur = hd.a0, a_n1 = hd.a1;
     float wa_cur = hd.wa0, wa_n1 = hd.wa1;
     v8i na0 = a_cur, na1 = a_n1;
     float nwa0 = 0.f, nwa1 = 0.f, nwb0 = 0.f;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const bool last = j + 1 == TM;
+    for (int j = 0; j < GR; ++j) {
+      const bool last = j + 1 == GR;
       v8i a_n2 = a_n1;
       float wa_n2 = wa_n1;
-      if (j + 2 < TM) {
-        a_n2 = frag(s.a, a_lo, a_hi, j + 2);
-        wa_n2 = s.sa[WM * wm + 16 * (j + 2) + l16];
+      if (j + 2 < GR) {
+        a_n2 = frag_a(s.a, j + 2);
+        wa_n2 = sap[kScaleStep * (j + 2)];
       } else if (last && kEarly) {
         __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt(0): slab kb fully read
         barrier();
-        na0 = frag(sn.a, a_lo, a_hi, 0);
-        nwa0 = sn.sa[WM * wm + l16];
+        na0 = frag_a(sn.a, 0);
+        nwa0 = row_scales(sn, kb + 1)[0];
         nwb0 = (MODE == kWgrad || kWbPerTile) ? 0.f : sn.sb[WN * wn];
-        na1 = frag(sn.a, a_lo, a_hi, TM > 1 ? 1 : 0);
-        nwa1 = sn.sa[WM * wm + (TM > 1 ? 16 : 0) + l16];
+        na1 = frag_a(sn.a, TM > 1 ? 1 : 0);
+        nwa1 = row_scales(sn, kb + 1)[TM > 1 ? kScaleStep : 0];
       }
       const float wj = MODE == kWgrad ? wa_cur : wa_cur * hd.wb0;
 #pragma unroll
@@ -1264,7 +1295,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
         // t = 0 folds the previous slab's last tile (before slab 0: a zero
         // partial of weight 0 into a zero accumulator, which changes nothing)
         if (t > 0) fold((t - 1) % TN, (t - 1) / TN);
-        else fold(TN - 1, TM - 1);
+        else fold(TN - 1, GR - 1);
         P_prev = P;
         pw = kWbPerTile ? wa_cur * hd.wbs[i] : wj;
         if (MODE == kWgrad) pwb = hd.wb[i];
@@ -1275,7 +1306,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
         }
       }
       if (!last || !kEarly) {
-        if (j + 2 < TM) __builtin_amdgcn_sched_group_barrier(0x0100, 3, 0); // DS reads
+        if (j + 2 < GR) __builtin_amdgcn_sched_group_barrier(0x0100, 3, 0); // DS reads
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x0008, 1, 0);               // one MFMA
@@ -1305,11 +1336,11 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   };
   // ---- tile end: fold the pending partial, store, start the next tile ------
   Origin org = tile_origin(0);
-  auto store_tile = [&]() {
+  auto store_tile = [&](auto groups) __attribute__((always_inline)) {
     const int64_t m0 = org.m0, n0 = org.n0;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int64_t row = m0 + WM * wm + 16 * j + l16;
+    for (int j = 0; j < decltype(groups)::value; ++j) {
+      const int64_t row = m0 + ra0 + kGroupRows * j;
       if (row >= M) continue;
       if (SPLIT) {
         float* prow = p.ws + ((int64_t)blockIdx.y * M + row) * N;
@@ -1341,10 +1372,10 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     }
   };
   int ti = 0, tkb = 0;
-  auto after_slab = [&]() {
+  auto after_slab = [&]() __attribute__((always_inline)) {
     if (!PERSIST || ++tkb < nslab) return;
     fold(TN - 1, TM - 1);
-    store_tile();
+    store_tile(std::integral_constant<int, TM>{});
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -1355,21 +1386,35 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     tkb = 0;
     if (++ti < my_tiles) org = tile_origin(ti);
   };
-  for (int u = 0; u < units; u += 3) {
-    slab(st0, st1);
-    after_slab();
-    if (u + 1 < units) {
-      slab(st1, st2);
+  auto run_groups = [&](auto groups) __attribute__((always_inline)) {
+    for (int u = 0; u < units; u += 3) {
+      slab(groups, u, st0, st1);
       after_slab();
+      if (u + 1 < units) {
+        slab(groups, u + 1, st1, st2);
+        after_slab();
+      }
+      if (u + 2 < units) {
+        slab(groups, u + 2, st2, st0);
+        after_slab();
+      }
     }
-    if (u + 2 < units) {
-      slab(st2, st0);
-      after_slab();
+    if (!PERSIST) {
+      fold(TN - 1, decltype(groups)::value - 1);
+      store_tile(groups);
     }
-  }
-  if (!PERSIST) {
-    fold(TN - 1, TM - 1);
-    store_tile();
+  };
+  if constexpr (VAR == kRagged) {
+    // only the groups that hold rows (at least one, so that every wave passes
+    // every barrier): a tile of 187 rows takes three quarters of a full one
+    static_assert(TM >= 2 && TM <= 4, "the cases below");
+    const int groups = ((int)(rt.rows + 15) / 16 - wm + WAVES_M - 1) / WAVES_M;
+    if (TM >= 4 && groups >= 4) run_groups(std::integral_constant<int, TM>{});
+    else if (TM >= 3 && groups >= 3) run_groups(std::integral_constant<int, TM < 3 ? TM : 3>{});
+    else if (groups >= 2) run_groups(std::integral_constant<int, 2>{});
+    else run_groups(std::integral_constant<int, 1>{});
+  } else {
+    run_groups(std::integral_constant<int, TM>{});
   }
 }
 
@@ -1487,28 +1532,29 @@ static int launch_ws_tiles(GemmArgs a, hipStream_t s) {
 }
 
 // Tile height for ragged segments: 64 (gemm_kernel, two workgroups per CU), 128,
-// 192 or 256 (warp-specialized), by rounds of the chip times what a round costs.
-// The rows' distribution is on the device; the estimate takes each expert that
-// can own rows two standard deviations (of a Poisson count) above the mean.
-// Costs per round (us over 32 blocks, measured with one tile per CU, and two
-// for the 64-row tiles).  Measured choices: 256 experts of 4096 x 7168 with 128
-// rows each 2.39 / 2.22 / 1.96 / 2.08 ms on 64 / 128 / 192 / 256 rows; 64 experts
-// of 7168 x 4096 (dgrad) with 187 rows 834 / 760 / 670 / 619 us; 256 experts of
-// 2048 x 2048 with 2 rows 157 / 196 us on 64 / 128 rows.
+// 192 or 256 (warp-specialized, one per CU), by what the tiles of all experts
+// cost.  The rows' distribution is on the device; the estimate takes each
+// expert that can own rows two standard deviations (of a Poisson count) above
+// the mean.  A warp-specialized tile costs 4 + 4.5 per 64 rows that it holds (us
+// over 32 blocks, measured; 11.5 or more, its weight slabs' copies); a round of
+// two 64-row tiles per CU costs 21.  Measured on 64 / 128 / 192 / 256 rows: 256
+// experts of 4096 x 7168 with 128 rows each 2.39 / 2.19 / 1.94 / 1.97 ms, 64 experts
+// of 7168 x 4096 (dgrad) with 187 rows 834 / 739 / 652 / 596 us, 256 experts of 2048 x
+// 2048 with 2 rows 158 / 190 / 195 / 230 us.
 static int ragged_tile_rows(int64_t rows, int64_t num_experts, int64_t n, int64_t cus) {
   const int64_t owners = num_experts < rows ? num_experts : rows;
   const double mean = (double)rows / (double)owners;
   const double high = owners == 1 ? mean : mean + 2.0 * sqrt(mean);
-  constexpr struct {
-    int bm, per_cu;
-    double cost;
-  } kTiles[] = {{64, 2, 21.0}, {128, 1, 13.0}, {192, 1, 17.5}, {256, 1, 22.0}};
+  const double strips = (double)owners * (double)(n / 128), chip = (double)cus;
+  auto tile = [](double r) { return fmax(11.5, 4.0 + 4.5 * ceil(r / 64.0)); };
   int best = 64;
-  double best_cost = 0.0;
-  for (const auto& t : kTiles) {
-    const double tiles = (double)owners * ceil(high / t.bm) * (double)(n / 128);
-    const double c = ceil(tiles / (double)(t.per_cu * cus)) * t.cost;
-    if (t.bm == 64 || c < best_cost) best = t.bm, best_cost = c;
+  double best_cost = ceil(strips * ceil(high / 64.0) / (2.0 * chip)) * 21.0;
+  for (int bm = 128; bm <= 256; bm += 64) {
+    const double full = floor(high / bm), rest = high - full * bm;
+    const double one = full > 0 ? tile(bm) : tile(rest);
+    const double all = full * tile(bm) + (rest > 0 ? tile(rest) : 0.0);
+    const double cost = fmax(one, strips * all / chip);
+    if (cost < best_cost) best = bm, best_cost = cost;
   }
   return best;
 }
@@ -1868,6 +1914,22 @@ extern "C" int fp8bs_gemm_wgrad(const uint8_t* qa, const float* sa, const uint8_
 // (a product that use_ws turns away has at most one such tile per CU).
 constexpr int64_t kTile128Cost = 23;
 
+// Whether 128 x 128 tiles beat the larger shapes of launch_gemm_ws (tile_cost's
+// measure: they cost 1.18 per unit of area, their patches reading more LDS per
+// MFMA, and win where the larger ones leave most of a round's CUs idle: dgrad
+// 1037x7168x1536 with a residual 26 -> 22 us, forward 1500x2048x7168 43 -> 33 us;
+// 3500x1536x4096, which stays on larger tiles, takes 29 us against 41).
+static bool epi_on_128(int64_t m, int64_t n, bool fwd, int cus) {
+  int64_t best = tile_cost(m, n, 256, 128, 100, cus);
+  const int64_t c192 = tile_cost(m, n, 192, 128, 110, cus);
+  if (c192 < best) best = c192;
+  if (fwd) {
+    const int64_t wide = tile_cost(m, n, 128, 192, 121, cus);
+    if (wide < best) best = wide;
+  }
+  return tile_cost(m, n, 128, 128, 118, cus) < best;
+}
+
 extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb,
                                    int64_t m, int64_t n, int64_t k, int b_layout, const float* bias, int act,
                                    const uint16_t* residual, int64_t ldr, uint16_t* z, int64_t ldz, uint16_t* c,
@@ -1882,11 +1944,15 @@ extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uin
   a.epi = Epilogue{bias, residual, ldr, z, ldz, act};
   hipStream_t s = (hipStream_t)stream;
   const int64_t cus = cu_count();
-  if (use_ws(m, n, false))
-    return b_layout == 0 ? launch_gemm_ws<kFprop, kEpi>(a, s, cus) : launch_gemm_ws<kDgrad, kEpi>(a, s, cus);
+  const bool fwd = b_layout == 0;
+  if (use_ws(m, n, false)) {
+    if (epi_on_128(m, n, fwd, cus))
+      return fwd ? launch_ws_tiles<kFprop, 128, kEpi>(a, s) : launch_ws_tiles<kDgrad, 128, kEpi>(a, s);
+    return fwd ? launch_gemm_ws<kFprop, kEpi>(a, s, cus) : launch_gemm_ws<kDgrad, kEpi>(a, s, cus);
+  }
   const SkinnyArgs sk{qa, sa, qb, sb, c, ldc, m, n, k, nullptr, 1, a.epi};
   if (skinny_cost(sk, b_layout, cus) <= kTile128Cost) return launch_skinny(sk, b_layout, cus, s);
-  return b_layout == 0 ? launch_ws_tiles<kFprop, 128, kEpi>(a, s) : launch_ws_tiles<kDgrad, 128, kEpi>(a, s);
+  return fwd ? launch_ws_tiles<kFprop, 128, kEpi>(a, s) : launch_ws_tiles<kDgrad, 128, kEpi>(a, s);
 }
 
 extern "C" int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets,
