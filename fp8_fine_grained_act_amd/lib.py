@@ -495,6 +495,15 @@ def _call(fn, dev, stream, *args):
         raise Fp8bsError(fn.__name__, status)
 
 
+def _empty(shape, dtype, device, stream):
+    """An output or workspace from the memory pool of the stream that the call runs on, so that its
+    memory is neither still in use by another stream nor handed to one while the call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _refuse(t, dtype, dev, name, what):
     _dev(t, dtype, name)
     if t.get_device() != dev:
@@ -545,7 +554,7 @@ def fp8bs_gemm_epilogue(qa, sa, qb, sb, b_layout=0, bias=None, act=FP8BS_ACT_NON
     if (rows if b_layout else cols) != k or sa.shape != (m, k // GROUP) or sb.shape != (rows // GROUP, cols // GROUP):
         raise ValueError("operand and scale shapes do not match")
     if c is None:
-        c = torch.empty((m, n), dtype=_bf16, device=qa.device)
+        c = _empty((m, n), _bf16, qa.device, stream)
     pc, ldc = _matrix(c, m, n, dev, "c")
     pr, ldr = (None, 0) if residual is None else _matrix(residual, m, n, dev, "residual")
     pz, ldz = (None, 0) if z is None else _matrix(z, m, n, dev, "z")
@@ -592,22 +601,20 @@ def fp8bs_epilogue_backward(dy, z, act=FP8BS_ACT_NONE, dz=None, dbias=None, accu
         dz = None
     else:
         if dz is None:
-            dz = torch.empty((m, n), dtype=_bf16, device=dy.device)
+            dz = _empty((m, n), _bf16, dy.device, stream)
         pdz, lddz = _matrix(dz, m, n, dev, "dz")
     if dbias is False:
         dbias = None
     else:
         if dbias is None:
-            dbias = torch.empty(n, dtype=_f32, device=dy.device)
+            dbias = _empty(n, _f32, dy.device, stream)
         pdb = _dense(dbias, _f32, dev, "dbias")
         if dbias.shape != (n,):
             raise ValueError("dbias must be [n]")
         if workspace is None:
             need = fp8bs_epilogue_backward_workspace(m, n)
             if need:
-                workspace = torch.empty(need // 4, dtype=_f32, device=dy.device)
-                if stream is not None:
-                    workspace.record_stream(stream)    # kept until that stream has used it
+                workspace = _empty(need // 4, _f32, dy.device, stream)
     if workspace is not None:
         pws, ws_bytes = _dense(workspace, _f32, dev, "workspace"), 4 * workspace.numel()
     _call(raw.fp8bs_epilogue_backward, dev, stream, pdy, ldy, pz, ldz, m, n, act, pdz, lddz, pdb, accumulate, pws,
@@ -629,11 +636,11 @@ def fp8bs_moe_route_ragged(topk_ids, num_experts, rows_cap=None, seg_offsets=Non
         rows_cap = tokens * topk
     on = topk_ids.device
     if seg_offsets is None:
-        seg_offsets = torch.empty(num_experts + 1, dtype=_i32, device=on)
+        seg_offsets = _empty(num_experts + 1, _i32, on, stream)
     if slot_rows is None:
-        slot_rows = torch.empty((tokens, topk), dtype=_i32, device=on)
+        slot_rows = _empty((tokens, topk), _i32, on, stream)
     if row_token is None:
-        row_token = torch.empty(rows_cap, dtype=_i32, device=on)
+        row_token = _empty(rows_cap, _i32, on, stream)
     pseg, pslot = _dense(seg_offsets, _i32, dev, "seg_offsets"), _dense(slot_rows, _i32, dev, "slot_rows")
     ptok = _dense(row_token, _i32, dev, "row_token")
     if seg_offsets.numel() != num_experts + 1 or slot_rows.shape != (tokens, topk) or row_token.numel() != rows_cap:
@@ -665,7 +672,7 @@ def fp8bs_grouped_gemm_ragged(qa, sa, seg_offsets, qb, sb, b_layout=0, c=None, s
     if seg_offsets.numel() != num_e + 1:
         raise ValueError("seg_offsets must have num_experts + 1 entries")
     if c is None:
-        c = torch.empty((rows, n), dtype=_bf16, device=qa.device)
+        c = _empty((rows, n), _bf16, qa.device, stream)
     pc, ldc = _matrix(c, rows, n, dev, "c")
     _call(raw.fp8bs_grouped_gemm_ragged, dev, stream, pqa, psa, pseg, num_e, rows, pqb, psb, n, k, b_layout, pc, ldc)
     return c
@@ -687,7 +694,7 @@ def fp8bs_grouped_wgrad_ragged(dy, x, seg_offsets, c=None, accumulate=0, stream=
     if c is None:
         if accumulate:
             raise ValueError("accumulate needs a c to add to")
-        c = torch.empty((num_e, m, n), dtype=_f32, device=dy.device)
+        c = _empty((num_e, m, n), _f32, dy.device, stream)
     pc = _dense(c, _f32, dev, "c")
     if c.shape != (num_e, m, n):
         raise ValueError("c must be [experts, m, n]")

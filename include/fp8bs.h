@@ -461,7 +461,8 @@ int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, c
  *       pointer and stride), otherwise must not overlap them
  *   dbias f32 [n] or NULL (not both NULL); accumulate == 1 adds to it
  *   workspace  at least fp8bs_epilogue_backward_workspace(m, n) bytes, used only
- *       by this call until it has run; may be NULL when that is 0 or dbias is NULL
+ *       by this call until it has run (two captured graphs that may run at once
+ *       need one each); may be NULL when that is 0 or dbias is NULL
  *   m >= 1 (any), n % 8 == 0.
  * Alignment: dy, z, dz 16 bytes, their strides % 8 == 0; dbias and workspace 4
  * bytes.  Errors: FP8BS_ERR_SCRATCH when the workspace is missing or too small.
@@ -493,7 +494,8 @@ int64_t fp8bs_epilogue_backward_workspace(int64_t m, int64_t n);
  * fp8bs_moe_route without padding rows: the same stable order, segments end to
  * end.  seg_offsets[num_experts] is the number of pairs kept; row_token [rows_cap]
  * is -1 from there on.  rows_cap >= tokens * topk; the other arguments, sizes and
- * errors as for fp8bs_moe_route.
+ * errors as for fp8bs_moe_route (slot_rows holds counts while the call runs, so
+ * it must not overlap any other argument).
  */
 int fp8bs_moe_route_ragged(const int32_t* topk_ids, int64_t tokens, int64_t topk, int64_t num_experts,
                            int32_t* seg_offsets, int32_t* slot_rows, int32_t* row_token, int64_t rows_cap,
@@ -525,7 +527,7 @@ int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t*
  *       expert's matrix (zeros for an empty segment), == 1 adds to it (an empty
  *       segment's matrix is not touched)
  *   1 <= num_experts <= 65536, 0 <= total_rows < 2^30 (0: dy and x may be NULL),
- *   m % 8 == 0, n % 8 == 0, ldy, ldx <= 2^24.
+ *   m % 8 == 0, n % 8 == 0, n <= 2^21, ldy, ldx <= 2^24.
  * Alignment: dy, x, c 16 bytes, ldy and ldx % 8 == 0, seg_offsets 4 bytes.
  */
 int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const uint16_t* x, int64_t ldx,

@@ -276,3 +276,22 @@ def test_epilogue_on_every_tile_shape(gpu_lib, m, n, k, b_layout):
     ey = SLOPE * ez + (argument(z64, "gelu_tanh") + 4) * 2.0 ** -24 * z64.abs()
     check(z, z64, ez, "z")
     check(c, y, ey + 2.0 ** -24 * (y.abs() + ey), "c")
+
+
+def test_backward_calls_at_once_on_two_streams(gpu_lib):
+    """Each call's outputs and workspace are its own, also where the call makes them."""
+    g = gen(17)
+    m, n = 9000, 1024
+    dy = [normal(g, m, n).bfloat16().cuda() for _ in range(2)]
+    z = normal(g, m, n).bfloat16().cuda()
+    want = [gpu_lib.fp8bs_epilogue_backward(d, z, act=ACTS["gelu_tanh"]) for d in dy]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dy]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            got[i].append(gpu_lib.fp8bs_epilogue_backward(dy[i], z, act=ACTS["gelu_tanh"], stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for dz, db in got[i]:
+            assert torch.equal(dz.view(torch.int16), want[i][0].view(torch.int16)) and torch.equal(db, want[i][1])

@@ -283,3 +283,27 @@ def test_every_tile_height(gpu_lib, low, high, n, b_layout):
         if cut.start < cut.stop:
             y, err = product64(dev[0][cut], dev[1][cut], dev[2][i], dev[3][i], b_layout)
             check(c[cut], y.cpu(), err.cpu(), f"expert {i}, {lengths[i]} rows")
+
+
+def test_large_routing_in_a_graph(gpu_lib):
+    """The three launches of a large routing, captured and replayed on other ids in the same buffers."""
+    g = gen(31)
+    tokens, topk, e = 3000, 5, 100
+    ids = torch.randint(-1, e + 1, (tokens, topk), generator=g, dtype=torch.int32).cuda()
+    out = gpu_lib.fp8bs_moe_route_ragged(ids, e)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gpu_lib.fp8bs_moe_route_ragged(ids, e, seg_offsets=out[0], slot_rows=out[1], row_token=out[2])
+    for _ in range(3):
+        ids.copy_(torch.randint(-1, e + 1, (tokens, topk), generator=g, dtype=torch.int32))
+        want = gpu_lib.fp8bs_moe_route_ragged(ids, e)
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+        rs, rl, rt = route_plain(ids.cpu().numpy(), e)
+        assert np.array_equal(out[0].cpu().numpy(), rs) and np.array_equal(out[1].cpu().numpy(), rl)
+        assert np.array_equal(out[2].cpu().numpy()[:len(rt)], rt)

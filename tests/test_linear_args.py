@@ -101,7 +101,8 @@ WG = dict(dy=P, ldy=16, x=P, ldx=24, seg=P, experts=4, rows=100, m=16, n=24, c=P
     (dict(rows=0, c=None), ENULL), (dict(accumulate=2), EFLAG),
     (dict(experts=0), ESHAPE), (dict(experts=65537), ESHAPE), (dict(rows=-1), ESHAPE), (dict(rows=1 << 30), ESHAPE),
     (dict(m=12), ESHAPE), (dict(n=20), ESHAPE), (dict(m=0), ESHAPE), (dict(ldy=8), ESHAPE), (dict(ldx=16), ESHAPE),
-    (dict(ldy=(1 << 24) + 8), ESHAPE), (dict(experts=65536, m=1 << 16, n=1 << 16, ldy=1 << 16, ldx=1 << 16), ESHAPE),
+    (dict(ldy=(1 << 24) + 8), ESHAPE), (dict(n=(1 << 21) + 8, ldx=(1 << 21) + 8), ESHAPE),
+    (dict(experts=65536, m=1 << 16, n=1 << 16, ldy=1 << 16, ldx=1 << 16), ESHAPE),
     (dict(dy=P + 8), EALIGN), (dict(x=P + 2), EALIGN), (dict(c=P + 4), EALIGN), (dict(ldy=20), EALIGN),
     (dict(ldx=28), EALIGN), (dict(seg=P + 1), EALIGN),
 ])
