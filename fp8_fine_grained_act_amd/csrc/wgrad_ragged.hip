@@ -23,10 +23,17 @@
 // Workgroups are persistent (one per CU, tiles w, w + G, ...) and their waves
 // have one role each.  Four copy waves keep a ring of three slabs filled across
 // tile boundaries.  The MFMA waves only read LDS, multiply and store: they wait
-// for no memory operation, so a tile's 4 BM BN bytes of output, which take about
-// as long to drain as a tile of 512 rows to multiply, leave under the next tiles.
-// (With every wave copying, a wave's copies wait behind its stores: 32 experts of
-// 4096 x 7168 with 512 rows each took 1.59 ms.)
+// for no memory operation.  (With every wave copying, a wave's copies wait behind its
+// stores: 32 experts of 4096 x 7168 with 512 rows each took 1.59 ms; 128 x 64 patches
+// on four MFMA waves 1.52 ms.)
+//
+// What bounds it: those 32 experts take 1.39 ms (0.69 PFLOP/s, 3.8 GB written); the
+// copies alone 0.61 ms (18 TB/s out of the L2s), LDS reads and MFMAs alone 0.73 ms
+// (1.3 PFLOP/s; 1.5 over long segments), the stores alone 0.69 ms (5.4 TB/s into HBM),
+// copies and stores without MFMAs 1.23 ms: the two hardly overlap, and that is the
+// bound.  Three of a wave's eight pieces of a tile therefore stay in registers and
+// leave one per slab under the next tile's MFMAs: 32 experts of 2048 x 2048 with 300
+// rows 152 -> 141 us, the sizes above 1.41 -> 1.39 ms.
 // Barrier u says that slab u has landed and that slab u - 1 has been read; the
 // copy waves then refill the stage of slab u - 1 with slab u + 2, and the MFMA
 // waves pass it in the last groups of slab u - 1, reading the first fragments
@@ -54,6 +61,7 @@ struct RaggedWgradArgs {
 
 constexpr int kT = 64;                         // rows of a slab: two MFMAs' contraction
 constexpr int kRing = 3;
+constexpr int kHeld = 3;                       // of a tile's 8 pieces per wave, stored under the next tile; 4 would spill
 constexpr int kBand = 4;                       // tile rows of a band: tiles walk down it, so the strips of dy
                                                // and x that are read at a time stay few
 
@@ -167,16 +175,13 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
 
   // ========================= MFMA waves ==========================================
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
-  // LDS offsets of the lane's words in slab 0: tile j of the wave's four, first
-  // read of k step 0; the second read lies 4 rows on, k step 1 32 rows on
+  // LDS offsets of the lane's words in slab 0: the first of the wave's four tiles
+  // (tile j at ^ (j << 5)), first read of k step 0; the second read lies 4 rows on,
+  // k step 1 32 rows on
   const int tl = 8 * g + (l16 >> 2);
-  uint32_t at_a[TM], at_b[TN];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_ptr_t*)lds;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    at_a[j] = lds0 + (uint32_t)(tl * BM * 2 + (((TM * wm + j) ^ tswz(tl)) << 5) + ((l16 & 3) << 3));
-    at_b[j] = lds0 + (uint32_t)(kSlabA + tl * BN * 2 + (((TN * wn + j) ^ tswz(tl)) << 5) + ((l16 & 3) << 3));
-  }
+  uint32_t at_a = (uint32_t)(tl * BM * 2 + (((TM * wm) ^ tswz(tl)) << 5) + ((l16 & 3) << 3));
+  uint32_t at_b = (uint32_t)(kSlabA + tl * BN * 2 + (((TN * wn) ^ tswz(tl)) << 5) + ((l16 & 3) << 3));
   auto frag = [&](uint32_t at, int row_bytes, int step) -> v8bf {
     v4i16 h[2];
 #pragma unroll
@@ -187,8 +192,8 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
     const v8i16 f = {h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]};
     return __builtin_bit_cast(v8bf, f);
   };
-  auto frag_a = [&](uint32_t stage, int j, int step) { return frag(at_a[j] + stage, BM * 2, step); };
-  auto frag_b = [&](uint32_t stage, int k, int step) { return frag(at_b[k] + stage, BN * 2, step); };
+  auto frag_a = [&](uint32_t stage, int j, int step) { return frag((at_a ^ (j << 5)) + (stage + lds0), BM * 2, step); };
+  auto frag_b = [&](uint32_t stage, int k, int step) { return frag((at_b ^ (k << 5)) + (stage + lds0), BN * 2, step); };
 
   v4f acc[TN][TM];
   auto clear = [&]() {
@@ -199,15 +204,82 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
   };
   clear();
 
+  // A patch is stored in 8 pieces of 16 rows by 32 columns (tiles j, k and k + 1):
+  // lanes 8 apart swap one tile's values for the other's, so that a store of 8
+  // rows writes whole 128-byte lines.
+  auto c_rsrc = [&](const Tile& t) {
+    return make_rsrc(p.c + (int64_t)t.e * p.m * p.n + t.m0 * p.n, min((int64_t)BM, p.m - t.m0) * p.n * 4);
+  };
+  const bool hi = l16 >= 8;
+  auto swap = [&](int j, int k, v4f (&o)[2]) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float send = hi ? acc[k][j][v] : acc[k + 1][j][v];
+      const float got = __uint_as_float(dpp_shuffle<0x128>(__float_as_uint(send)));
+      o[0][v] = hi ? got : acc[k][j][v];
+      o[1][v] = hi ? acc[k + 1][j][v] : got;
+    }
+  };
+  // rows past m end behind the range, columns past n are sent there
+  auto put = [&](__amdgpu_buffer_rsrc_t rc, int64_t n0, int j, int k, int h, v4f o) {
+    const int row = 64 * wm + 16 * j + (l16 & 7) + 8 * h;
+    const uint32_t col = (uint32_t)n0 + 64 * wn + 16 * k + (hi ? 16 : 0) + 4 * g;
+    const uint32_t off = col < (uint32_t)p.n ? ((uint32_t)row * (uint32_t)p.n + col) * 4u : 0xFFFFFFF0u;
+    if (p.accumulate) {
+      const v4f old = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off, 0, 0));
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] += old[v];
+    }
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), rc, (int)off, 0, STREAM ? 2 : 0);
+  };
+  auto store = [&](const Tile& t, int u0) {
+    const __amdgpu_buffer_rsrc_t rc = c_rsrc(t);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+#pragma unroll
+      for (int k = 0; k < TN; k += 2) {
+        if (2 * j + k / 2 < u0) continue;
+        v4f o[2];
+        swap(j, k, o);
+        put(rc, t.n0, j, k, 0, o[0]);
+        put(rc, t.n0, j, k, 1, o[1]);
+      }
+    }
+  };
+  // The first kHeld pieces of a finished tile wait in registers and are stored one
+  // per slab under the next tile's MFMAs.
+  v4f held[kHeld][2];
+  int pending = 0;
+  Tile held_t;
+  auto hold = [&](const Tile& t) {
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) swap(u / 2, u % 2 * 2, held[u]);
+    pending = kHeld;
+    held_t = t;
+  };
+  auto drip = [&]() {
+    if (pending == 0) return;
+    --pending;
+    const __amdgpu_buffer_rsrc_t rc = c_rsrc(held_t);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+      if (pending == u) {
+        put(rc, held_t.n0, u / 2, u % 2 * 2, 0, held[u][0]);
+        put(rc, held_t.n0, u / 2, u % 2 * 2, 1, held[u][1]);
+      }
+  };
+
   // Groups of one A fragment and its four MFMAs; A fragments are read kAhead
-  // groups ahead of them.
-  constexpr int kGroups = 2 * TM, kAhead = 3;
+  // groups ahead of them (the other wave of the SIMD covers what that leaves).
+  constexpr int kGroups = 2 * TM, kAhead = 1;
   v8bf bf[2][TN], af[kAhead + 1];
   uint32_t stage = 0;                          // byte offset of the current slab's stage
   auto slab = [&](bool more) {
+    asm("" : "+v"(at_a), "+v"(at_b));          // the four tiles' offsets are not kept in registers
     const uint32_t next = stage == (kRing - 1) * kSlab ? 0 : stage + kSlab;
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
+      if (q == 5) drip();
       const int step = q / TM, j = q % TM, n = q + kAhead;
       if (q < TN) bf[1][q] = frag_b(stage, q, 1);
       if (n < kGroups) {
@@ -228,40 +300,6 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
     }
     stage = next;
   };
-  auto store = [&](const Tile& t) {
-    const __amdgpu_buffer_rsrc_t rc =
-        make_rsrc(p.c + (int64_t)t.e * p.m * p.n + t.m0 * p.n, min((int64_t)BM, p.m - t.m0) * p.n * 4);
-    const bool hi = l16 >= 8;
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-#pragma unroll
-      for (int k = 0; k < TN; k += 2) {
-        // lanes 8 apart swap one tile's piece for the other's, so that a store
-        // writes whole 128-byte lines (8 rows of 32 columns)
-        v4f o[2];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float send = hi ? acc[k][j][v] : acc[k + 1][j][v];
-          const float got = __uint_as_float(dpp_shuffle<0x128>(__float_as_uint(send)));
-          o[0][v] = hi ? got : acc[k][j][v];
-          o[1][v] = hi ? acc[k + 1][j][v] : got;
-        }
-        const int row = 64 * wm + 16 * j + (l16 & 7);
-        const int64_t col = t.n0 + 64 * wn + 16 * k + (hi ? 16 : 0) + 4 * g;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // rows past m end behind the range, columns past n are sent there
-          const uint32_t off = col < p.n ? (uint32_t)(((int64_t)(row + 8 * h) * p.n + col) * 4) : 0xFFFFFFF0u;
-          if (p.accumulate) {
-            const v4f old = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)off, 0, 0));
-#pragma unroll
-            for (int v = 0; v < 4; ++v) o[h][v] += old[v];
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[h]), rc, (int)off, 0, STREAM ? 2 : 0);
-        }
-      }
-    }
-  };
 
   Tile live = live_tile(first);
   if (live.i < total) {
@@ -276,10 +314,16 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
       const Tile t = live;
       live = live_tile(i + G);
       for (int s = 0; s < t.slabs; ++s) slab(s + 1 < t.slabs || live.i < total);
-      store(t);
+      while (pending) drip();
+      if (live.i < total && !p.accumulate) {
+        hold(t);
+        store(t, kHeld);
+      } else {
+        store(t, 0);
+      }
       clear();
     } else if (!p.accumulate) {
-      store(tile_at(i));                       // no rows: zeros
+      store(tile_at(i), 0);                    // no rows: zeros
     }
   }
 }

@@ -307,3 +307,23 @@ def test_large_routing_in_a_graph(gpu_lib):
         rs, rl, rt = route_plain(ids.cpu().numpy(), e)
         assert np.array_equal(out[0].cpu().numpy(), rs) and np.array_equal(out[1].cpu().numpy(), rl)
         assert np.array_equal(out[2].cpu().numpy()[:len(rt)], rt)
+
+
+def test_wgrad_many_tiles(gpu_lib):
+    """More tiles than workgroups, so that tiles follow one another: short, long and empty segments in turn."""
+    g = gen(77)
+    lengths = [1, 300, 0, 64, 65, 0, 0, 130, 5, 200] * 8
+    e, m, n = len(lengths), 520, 1032
+    seg = seg_of(lengths)
+    dy, x = normal(g, int(seg[-1]), m).bfloat16().cuda(), normal(g, int(seg[-1]), n).bfloat16().cuda()
+    base = torch.randn((e, m, n), device="cuda")
+    c = torch.full((e, m, n), float("nan"), device="cuda")
+    gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg.cuda(), c=c)
+    acc = gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg.cuda(), c=base.clone(), accumulate=1)
+    torch.cuda.synchronize()
+    for i in range(e):
+        a, b = dy[int(seg[i]):int(seg[i + 1])].double(), x[int(seg[i]):int(seg[i + 1])].double()
+        want, err = (a.t() @ b).cpu(), (2.0 ** -23 * (lengths[i] + 2) * (a.abs().t() @ b.abs())).cpu()
+        check(c[i], want, err, f"expert {i}", bf16=False)
+        tot = base[i].double().cpu() + want
+        check(acc[i], tot, err + 2.0 ** -24 * (tot.abs() + err), f"expert {i} accumulated", bf16=False)
