@@ -147,6 +147,14 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   return u >> 16;
 }
 
+// Two values at once in the hardware's conversion (v_cvt_pk_bf16_f32, to nearest
+// even too, NaN kept): lo in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2bf));
+}
+
 // ---- a linear layer's epilogue -----------------------------------------------
 // C = act(z) + residual, z = product + bias.
 struct Epilogue {
@@ -180,7 +188,7 @@ __device__ __forceinline__ float gelu_clip(float z) { return __builtin_amdgcn_fm
 __device__ __forceinline__ void act_forward4(int act, float (&z)[4]) {
   if (act == FP8BS_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = fmaxf(z[i], 0.0f);
+    for (int i = 0; i < 4; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];     // NaN stays
   } else if (act == FP8BS_ACT_GELU_TANH) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -198,7 +206,7 @@ template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == FP8BS_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if (ACT == FP8BS_ACT_GELU_TANH) {
-    const float c = gelu_clip(z), cc = c * c;
+    const float c = z == z ? gelu_clip(z) : z, cc = c * c;   // the clip alone would drop a NaN
     const float p = sigmoid_of(c * __builtin_fmaf(kGeluC1, cc, kGeluC0));
     return __builtin_fmaf(c * p * (1.0f - p), __builtin_fmaf(3.0f * kGeluC1, cc, kGeluC0), p);
   }

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
           const float hi = bf16_hi(dd[i]) * act_slope<ACT>(bf16_hi(zz[i]));
           sum[2 * i] += lo;
           sum[2 * i + 1] += hi;
-          o[i] = f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
+          o[i] = pack_bf16(lo, hi);
         }
         if (!p.dz) continue;
         uint16_t* const dst = p.dz + row * p.lddz + col;

@@ -29,10 +29,7 @@ __device__ __forceinline__ void finish4(const SkinnyArgs& p, int64_t row, int64_
 #pragma unroll
     for (int v = 0; v < 4; ++v) x[v] += ep.bias[col + v];
   }
-  auto pack = [&]() {
-    return make_uint2(f32_to_bf16_rne(x[0]) | (f32_to_bf16_rne(x[1]) << 16),
-                      f32_to_bf16_rne(x[2]) | (f32_to_bf16_rne(x[3]) << 16));
-  };
+  auto pack = [&]() { return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])); };
   if (ep.z) *reinterpret_cast<uint2*>(ep.z + row * ep.ldz + col) = pack();
   act_forward4(ep.act, x);
   if (ep.res) {

@@ -452,7 +452,7 @@ int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, c
 /*
  * The epilogue's backward pass, from one read of dy and z:
  *   dz[i, j] = dy[i, j] act'(z[i, j])  (bf16),   dbias[j] (+)= sum_i dz[i, j]  (f32)
- * act' is taken at the stored bf16 z; relu'(0) = 0.  dbias sums the FP32 dz,
+ * act' is taken at the stored bf16 z; relu'(0) = 0 (and 0 at NaN).  dbias sums the FP32 dz,
  * before its rounding, in an order that depends on (m, n) only.  The residual's
  * gradient is dy.
  *   dy  bf16 [m, n], row stride ldy      z  bf16 [m, n], row stride ldz (may be

@@ -295,3 +295,41 @@ def test_backward_calls_at_once_on_two_streams(gpu_lib):
     for i in range(2):
         for dz, db in got[i]:
             assert torch.equal(dz.view(torch.int16), want[i][0].view(torch.int16)) and torch.equal(db, want[i][1])
+
+
+def test_not_a_number_stays_one(gpu_lib):
+    """NaN and infinities of a row reach that row's outputs and its columns' sums, and nothing else."""
+    m, n = 70, 1024
+    g = gen(23)
+    dy, z = normal(g, m, n).bfloat16(), normal(g, m, n).bfloat16()
+    clean = gpu_lib.fp8bs_epilogue_backward(dy.cuda(), z.cuda(), act=ACTS["silu"])
+    nan = torch.tensor([0x7FFF], dtype=torch.int16).view(torch.bfloat16)       # the payload that an integer rounding loses
+    dy[3, 5], dy[4, 6], dy[5, 7] = nan[0], float("inf"), float("-inf")
+    dz, db = gpu_lib.fp8bs_epilogue_backward(dy.cuda(), z.cuda(), act=ACTS["silu"])
+    torch.cuda.synchronize()
+    assert torch.isnan(dz[3, 5]) and torch.isnan(db[5]) and torch.isinf(dz[4, 6]) and torch.isinf(db[6]) and torch.isinf(db[7])
+    keep = torch.ones((m, n), dtype=torch.bool)
+    keep[3, 5] = keep[4, 6] = keep[5, 7] = False
+    assert torch.equal(dz.cpu()[keep], clean[0].cpu()[keep])
+    cols = torch.ones(n, dtype=torch.bool)
+    cols[5:8] = False
+    assert torch.equal(db.cpu()[cols], clean[1].cpu()[cols])
+    # the forward: a NaN bias column and a NaN residual value
+    qa, sa = row_tiles(normal(g, m, 256))
+    qb, sb = blocks(normal(g, n, 256) * 0.05)
+    dev = [t.cuda() for t in (qa, sa, qb, sb)]
+    bias, res = torch.zeros(n), torch.zeros((m, n), dtype=torch.bfloat16)
+    y0 = gpu_lib.fp8bs_gemm_epilogue(*dev, bias=bias.cuda(), act=ACTS["gelu_tanh"], residual=res.cuda()).cpu()
+    bias[9], res[2, 11] = float("nan"), nan[0]
+    y = gpu_lib.fp8bs_gemm_epilogue(*dev, bias=bias.cuda(), act=ACTS["gelu_tanh"], residual=res.cuda()).cpu()
+    assert torch.isnan(y[:, 9]).all() and torch.isnan(y[2, 11])
+    keep = torch.ones((m, n), dtype=torch.bool)
+    keep[:, 9] = keep[2, 11] = False
+    assert torch.equal(y[keep], y0[keep])
+    # a NaN pre-activation: no activation hides it, and the smooth slopes keep it
+    for act in ("relu", "gelu_tanh", "silu"):
+        y = gpu_lib.fp8bs_gemm_epilogue(*dev, bias=bias.cuda(), act=ACTS[act]).cpu()
+        assert torch.isnan(y[:, 9]).all() and int(torch.isnan(y).sum()) == m, act
+    for act in ("gelu_tanh", "silu"):
+        dz, _ = gpu_lib.fp8bs_epilogue_backward(torch.ones_like(z).cuda(), torch.full_like(z, float("nan")).cuda(), act=ACTS[act])
+        assert torch.isnan(dz).all(), act
