@@ -67,7 +67,8 @@ constexpr int kBand = 4;                       // tile rows of a band: tiles wal
 
 __device__ __forceinline__ int tswz(int t) { return (t & 3) | ((t >> 1) & 4); }
 
-template <int BM, int BN, bool STREAM>
+// SPLIT: each segment's slabs in gridDim.y parts, c holds [gridDim.y][num_experts][m][n].
+template <int BM, int BN, bool STREAM, bool SPLIT = false>
 __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_kernel(RaggedWgradArgs p) {
   constexpr int WAVES_N = BN / 64, MW = BM / 64 * WAVES_N, TM = 4, TN = 4;      // 64 x 64 patches
   constexpr int kSlabA = kT * BM * 2, kSlab = kSlabA + kT * BN * 2;
@@ -100,6 +101,14 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
     t.s0 = min(max(p.seg[t.e], 0), cap);
     t.rows = max(0, min(max(p.seg[t.e + 1], 0), cap) - t.s0);
     t.slabs = (t.rows + kT - 1) / kT;
+    if (SPLIT) {                               // part blockIdx.y of the segment's slabs
+      const uint32_t all = (uint32_t)t.slabs, y = blockIdx.y;
+      const int lo = __builtin_amdgcn_readfirstlane((int)(y * all / gridDim.y));
+      const int hi = __builtin_amdgcn_readfirstlane((int)((y + 1) * all / gridDim.y));
+      t.rows = min(t.rows, hi * kT) - lo * kT;
+      t.s0 += lo * kT;
+      t.slabs = hi - lo;
+    }
     return t;
   };
   // the first tile from i on that has rows
@@ -208,7 +217,7 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
   // lanes 8 apart swap one tile's values for the other's, so that a store of 8
   // rows writes whole 128-byte lines.
   auto c_rsrc = [&](const Tile& t) {
-    return make_rsrc(p.c + (int64_t)t.e * p.m * p.n + t.m0 * p.n, min((int64_t)BM, p.m - t.m0) * p.n * 4);
+    return make_rsrc(p.c + (SPLIT ? blockIdx.y * p.num_experts + t.e : (int64_t)t.e) * p.m * p.n + t.m0 * p.n, min((int64_t)BM, p.m - t.m0) * p.n * 4);
   };
   const bool hi = l16 >= 8;
   auto swap = [&](int j, int k, v4f (&o)[2]) {
@@ -328,13 +337,76 @@ __global__ __launch_bounds__(64 * (BM / 64 * (BN / 64) + 4)) void ragged_wgrad_k
   }
 }
 
+// c (+)= the parts' sums in order; with accumulate, an empty segment's matrix is not touched.
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ parts, int64_t splits,
+                                                         const int32_t* __restrict__ seg, int64_t num_experts, int cap,
+                                                         int64_t mn, float* __restrict__ c, int accumulate) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, e = blockIdx.y;
+  if (i >= mn) return;
+  if (accumulate && min(max(seg[e + 1], 0), cap) <= min(max(seg[e], 0), cap)) return;
+  const float* src = parts + e * mn + i;
+  float4 s = *reinterpret_cast<const float4*>(src);
+  for (int64_t k = 1; k < splits; ++k) {
+    const float4 o = *reinterpret_cast<const float4*>(src + k * num_experts * mn);
+    s.x += o.x;
+    s.y += o.y;
+    s.z += o.z;
+    s.w += o.w;
+  }
+  float4* const dst = reinterpret_cast<float4*>(c + e * mn + i);
+  if (accumulate) {
+    const float4 o = *dst;
+    s.x += o.x;
+    s.y += o.y;
+    s.z += o.z;
+    s.w += o.w;
+  }
+  *dst = s;
+}
+
+// Parts of the contraction: 1 unless the tiles fill at most half the CUs and the mean
+// segment is 48 slabs or more; then as many as fill the CUs, each with 8 slabs or more of
+// the mean segment, at most 32.  (The rows' distribution is on the device.)  A slab
+// takes 0.7 us there, the stream-ordered workspace and the joining launch about 15: one
+// expert of 512 x 512 with 4096 rows 47 -> 27 us, of 256 x 256 with 32768 rows 323 -> 32,
+// of 2048 x 2048 with 4096 rows (two parts) 51 either way; shorter ones lose (four
+// of 512 x 512 with 2048 rows 27.6 against 27, one of 1536 x 1536 with 1024 rows 19
+// against 30).
+static int64_t wgrad_splits(const RaggedWgradArgs& a, int64_t tiles, int64_t cus) {
+  const int64_t slabs = a.total_rows / (a.num_experts * kT);
+  if (2 * tiles > cus || slabs < 48) return 1;
+  int64_t s = cus / tiles;
+  if (s > slabs / 8) s = slabs / 8;
+  return s < 32 ? s : 32;
+}
+
 template <int BM, int BN>
 static int launch_ragged_wgrad(RaggedWgradArgs a, int64_t cus, hipStream_t s) {
   a.tiles_m = (a.m + BM - 1) / BM;
   a.tiles_n = (a.n + BN - 1) / BN;
   const int64_t total = a.num_experts * a.tiles_m * a.tiles_n;
   if (total > kMaxGrid) return FP8BS_ERR_SHAPE;
-  const dim3 g((unsigned)(total < cus ? total : cus)), b(64 * (BM / 64 * (BN / 64) + 4));
+  const int64_t splits = wgrad_splits(a, total, cus), mn = a.m * a.n;
+  const dim3 b(64 * (BM / 64 * (BN / 64) + 4));
+  if (splits > 1) {
+    void* ws = nullptr;
+    if (hipMallocAsync(&ws, (size_t)(splits * a.num_experts * mn * 4), s) == hipSuccess) {
+      RaggedWgradArgs parts = a;
+      parts.c = static_cast<float*>(ws);
+      parts.accumulate = 0;
+      hipLaunchKernelGGL((ragged_wgrad_kernel<BM, BN, false, true>), dim3((unsigned)total, (unsigned)splits), b, 0, s, parts);
+      int st = launch_status();
+      if (st == FP8BS_OK) {
+        hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)((mn / 4 + 255) / 256), (unsigned)a.num_experts), dim3(256), 0,
+                           s, parts.c, splits, a.seg, a.num_experts, (int)a.total_rows, mn, a.c, a.accumulate);
+        st = launch_status();
+      }
+      if (hipFreeAsync(ws, s) != hipSuccess && st == FP8BS_OK) st = FP8BS_ERR_LAUNCH;
+      return st;
+    }
+    (void)hipGetLastError();                   // no memory for the parts: unsplit
+  }
+  const dim3 g((unsigned)(total < cus ? total : cus));
   if (a.num_experts * a.m * a.n * 4 > kStreamBytes)
     hipLaunchKernelGGL((ragged_wgrad_kernel<BM, BN, true>), g, b, 0, s, a);
   else

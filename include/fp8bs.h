@@ -526,6 +526,10 @@ int fp8bs_grouped_gemm_ragged(const uint8_t* qa, const float* sa, const int32_t*
  *   c   f32 [num_experts, m, n] contiguous; accumulate == 0 overwrites every
  *       expert's matrix (zeros for an empty segment), == 1 adds to it (an empty
  *       segment's matrix is not touched)
+ * Few outputs over long segments split the rows: FP32 partial sums in a stream-ordered
+ * workspace on the call's stream, added in a fixed order (without memory for it the
+ * call runs unsplit, to the same bound with other bits).  The bits depend on the sizes
+ * and the segments only, on one kind of device.
  *   1 <= num_experts <= 65536, 0 <= total_rows < 2^30 (0: dy and x may be NULL),
  *   m % 8 == 0, n % 8 == 0, n <= 2^21, ldy, ldx <= 2^24.
  * Alignment: dy, x, c 16 bytes, ldy and ldx % 8 == 0, seg_offsets 4 bytes.

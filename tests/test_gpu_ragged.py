@@ -327,3 +327,41 @@ def test_wgrad_many_tiles(gpu_lib):
         check(c[i], want, err, f"expert {i}", bf16=False)
         tot = base[i].double().cpu() + want
         check(acc[i], tot, err + 2.0 ** -24 * (tot.abs() + err), f"expert {i} accumulated", bf16=False)
+
+
+@pytest.mark.parametrize("lengths,m,n", [([4096], 256, 136), ([3000, 0, 1090], 72, 200), ([1024, 5, 1, 4097], 264, 128)])
+def test_wgrad_split_over_rows(gpu_lib, lengths, m, n):
+    """Few tiles over long segments: the rows are split and the parts joined, the same bits every time."""
+    g, e = gen(m + n), len(lengths)
+    seg = seg_of(lengths)
+    dy, x = normal(g, int(seg[-1]), m).bfloat16().cuda(), normal(g, int(seg[-1]), n).bfloat16().cuda()
+    base = torch.randn((e, m, n), device="cuda")
+    base[:, 0, 0] = -0.0
+    c = gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg.cuda())
+    acc = gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg.cuda(), c=base.clone(), accumulate=1)
+    torch.cuda.synchronize()
+    for i in range(e):
+        a, b = dy[int(seg[i]):int(seg[i + 1])].double(), x[int(seg[i]):int(seg[i + 1])].double()
+        want, err = (a.t() @ b).cpu(), (2.0 ** -23 * (lengths[i] + 2) * (a.abs().t() @ b.abs())).cpu()
+        check(c[i], want, err, f"expert {i}", bf16=False)
+        tot = base[i].double().cpu() + want
+        check(acc[i], tot, err + 2.0 ** -24 * (tot.abs() + err), f"expert {i} accumulated", bf16=False)
+        if lengths[i] == 0:
+            assert torch.equal(acc[i].view(torch.int32), base[i].view(torch.int32))
+    # on another stream, and captured and replayed on other rows
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    d = gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg.cuda(), stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(c, d)
+    seg_d, out = seg.cuda(), torch.empty_like(c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg_d, c=out)
+    for i in range(4):
+        dy.copy_(dy.roll(i + 1, 0))
+        want = gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg_d)
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
