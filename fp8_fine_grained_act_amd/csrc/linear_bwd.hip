@@ -4,7 +4,7 @@
 //
 // (the residual's gradient is dy itself).  dz goes on to the quantizers and the
 // dgrad and wgrad products.  One pass over dy and z, bound by HBM (6 bytes per
-// element): a workgroup owns a strip of 512 columns and a run of rows, wave w
+// element): a workgroup owns a strip of columns and a run of rows, wave w
 // taking rows w, w + kBwdWaves, ...; each lane sums its 8 columns' FP32 dz in
 // registers, the waves' sums meet in LDS in wave order.  With one run of rows
 // the workgroup writes dbias itself; otherwise its sums go to the caller's
@@ -40,11 +40,13 @@ struct BwdArgs {
 
 // STREAM: the call's bytes are larger than half the last-level cache, and pass
 // through with the non-temporal hint.
-template <int ACT, bool STREAM>
+// LPR: lanes per row, 64 (strips of 512 columns) or 8 (strips of 64, a wave's step 8 rows).
+template <int ACT, bool STREAM, int LPR>
 __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p) {
-  __shared__ float part[kBwdWaves][512];
+  constexpr int kCols = 8 * LPR, kRows = 64 / LPR;
+  __shared__ float part[kBwdWaves][kCols];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 512 + 8 * lane;
+  const int64_t col = (int64_t)blockIdx.x * kCols + 8 * (lane % LPR);
   const bool live = col < p.n;
   const int64_t r0 = (int64_t)blockIdx.y * p.run_rows;
   const int64_t r1 = min(p.m, r0 + p.run_rows);
@@ -54,11 +56,11 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
 
   if (live) {
-    for (int64_t r = r0 + wave; r < r1; r += kBwdWaves * kBwdUnroll) {
+    for (int64_t r = r0 + wave * kRows + lane / LPR; r < r1; r += kBwdWaves * kRows * kBwdUnroll) {
       uint4 d[kBwdUnroll], zv[kBwdUnroll];
 #pragma unroll
       for (int u = 0; u < kBwdUnroll; ++u) {
-        const int64_t row = r + u * kBwdWaves;
+        const int64_t row = r + u * kBwdWaves * kRows;
         d[u] = zv[u] = make_uint4(0, 0, 0, 0);
         if (row < r1) {
           d[u] = load(p.dy + row * p.ldy + col);
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
       }
 #pragma unroll
       for (int u = 0; u < kBwdUnroll; ++u) {
-        const int64_t row = r + u * kBwdWaves;
+        const int64_t row = r + u * kBwdWaves * kRows;
         if (row >= r1) break;
         const uint32_t dd[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
         const uint32_t zz[4] = {zv[u].x, zv[u].y, zv[u].z, zv[u].w};
@@ -89,10 +91,16 @@ __global__ __launch_bounds__(64 * kBwdWaves) void epilogue_bwd_kernel(BwdArgs p)
   }
   if (!p.sums) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[wave][8 * lane + i] = sum[i];
+  for (int d = LPR; d < 64; d <<= 1)           // the wave's rows
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor(sum[i], d);
+  if (lane < LPR) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[wave][8 * lane + i] = sum[i];
+  }
   __syncthreads();
-  for (int c = threadIdx.x; c < 512; c += 64 * kBwdWaves) {
-    const int64_t j = (int64_t)blockIdx.x * 512 + c;
+  for (int c = threadIdx.x; c < kCols; c += 64 * kBwdWaves) {
+    const int64_t j = (int64_t)blockIdx.x * kCols + c;
     if (j >= p.n) continue;
     float s = part[0][c];
 #pragma unroll
@@ -121,8 +129,15 @@ __global__ __launch_bounds__(1024) void bias_sum_kernel(const float* __restrict_
   }
 }
 
+// Up to here a workgroup takes all rows of a strip of 64 columns: one launch and no
+// workspace, which saves a short call's host time too (on strips of 512 columns against these:
+// 37 x 1536 4.5 and 3.1 us on the device, 256 x 4096 8.4 and 4.7, 15.3 and 10.7 with
+// the host's call, 512 x 16384 12.3 and 10.1; at 1024 rows the two launches win).
+constexpr int64_t kNarrowRows = 512;
+
 // Rows per run: about 512 workgroups over the strips, 64 rows or more each.
 static int64_t bwd_run_rows(int64_t m, int64_t n) {
+  if (m <= kNarrowRows) return m;
   const int64_t strips = (n + 511) / 512;
   const int64_t want = strips < 512 ? 512 / strips : 1;
   int64_t rows = (m + want - 1) / want;
@@ -135,11 +150,16 @@ static int64_t bwd_runs(int64_t m, int64_t n) { return (m + bwd_run_rows(m, n) -
 
 template <int ACT>
 static void launch_bwd(const BwdArgs& a, int64_t runs, hipStream_t s) {
+  if (a.m <= kNarrowRows) {
+    const dim3 strips((unsigned)((a.n + 63) / 64)), threads(64 * kBwdWaves);
+    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, false, 8>), strips, threads, 0, s, a);
+    return;
+  }
   const dim3 grid((unsigned)((a.n + 511) / 512), (unsigned)runs), block(64 * kBwdWaves);
   if (6 * a.m * a.n > kStreamBytes)
-    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, true, 64>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((epilogue_bwd_kernel<ACT, false, 64>), grid, block, 0, s, a);
 }
 
 }  // namespace fp8bs

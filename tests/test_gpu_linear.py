@@ -333,3 +333,18 @@ def test_not_a_number_stays_one(gpu_lib):
     for act in ("gelu_tanh", "silu"):
         dz, _ = gpu_lib.fp8bs_epilogue_backward(torch.ones_like(z).cuda(), torch.full_like(z, float("nan")).cuda(), act=ACTS[act])
         assert torch.isnan(dz).all(), act
+
+
+@pytest.mark.parametrize("m,n", [(511, 200), (512, 1032), (513, 64), (300, 4096), (9, 65544)])
+def test_backward_around_the_row_limit_of_one_launch(gpu_lib, m, n):
+    g = gen(m)
+    dy, z = (normal(g, m, n) * 1e-2).bfloat16(), (normal(g, m, n) * 2).bfloat16()
+    base = normal(g, n)
+    db = base.cuda()
+    assert (gpu_lib.fp8bs_epilogue_backward_workspace(m, n) == 0) == (m <= 512)
+    dz, _ = gpu_lib.fp8bs_epilogue_backward(dy.cuda(), z.cuda(), act=ACTS["gelu_tanh"], dbias=db, accumulate=1)
+    torch.cuda.synchronize()
+    dz64, e, db64, eb = bwd64(dy, z, "gelu_tanh")
+    check(dz, dz64, e, "dz")
+    tot = base.double() + db64
+    check(db, tot, eb + 2.0 ** -24 * (tot.abs() + eb), "dbias", bf16=False)
