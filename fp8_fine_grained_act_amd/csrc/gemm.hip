@@ -259,16 +259,22 @@ __device__ __forceinline__ void store_pair(uint16_t* dst, const float (&x)[4], c
     *reinterpret_cast<uint4*>(dst) = v;
 }
 
-template <int TN, int TM>
+// Ragged segments round in the hardware's conversion, as the few-row tiles do
+// (skinny.hip), so that a NaN stays one whatever tile its row falls into; finite
+// values and infinities round to the same bits either way.
+template <int VAR, int TN, int TM>
 __device__ __forceinline__ void store_row_bf16(const GemmArgs& p, const v4f (&acc)[TN][TM], int j, int64_t row,
                                                int64_t col0, int g) {
   uint16_t* const crow = reinterpret_cast<uint16_t*>(p.c) + row * p.ldc;
+  auto pack = [](float lo, float hi) {
+    return VAR == kRagged ? pack_bf16(lo, hi) : f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
+  };
 #pragma unroll
   for (int i = 0; i + 1 < TN; i += 2) {
-    const uint32_t x0 = f32_to_bf16_rne(acc[i][j][0]) | (f32_to_bf16_rne(acc[i][j][1]) << 16);
-    const uint32_t x1 = f32_to_bf16_rne(acc[i][j][2]) | (f32_to_bf16_rne(acc[i][j][3]) << 16);
-    const uint32_t y0 = f32_to_bf16_rne(acc[i + 1][j][0]) | (f32_to_bf16_rne(acc[i + 1][j][1]) << 16);
-    const uint32_t y1 = f32_to_bf16_rne(acc[i + 1][j][2]) | (f32_to_bf16_rne(acc[i + 1][j][3]) << 16);
+    const uint32_t x0 = pack(acc[i][j][0], acc[i][j][1]);
+    const uint32_t x1 = pack(acc[i][j][2], acc[i][j][3]);
+    const uint32_t y0 = pack(acc[i + 1][j][0], acc[i + 1][j][1]);
+    const uint32_t y1 = pack(acc[i + 1][j][2], acc[i + 1][j][3]);
     const auto s0 = __builtin_amdgcn_permlane16_swap(x0, y0, false, false);
     const auto s1 = __builtin_amdgcn_permlane16_swap(x1, y1, false, false);
     const int64_t col = col0 + 16 * i + 16 * (g & 1) + 8 * (g >> 1);
@@ -284,8 +290,8 @@ __device__ __forceinline__ void store_row_bf16(const GemmArgs& p, const v4f (&ac
     const int64_t col = col0 + 16 * (TN - 1) + 4 * g;
     if (col < p.n) {
       uint2 o;
-      o.x = f32_to_bf16_rne(acc[TN - 1][j][0]) | (f32_to_bf16_rne(acc[TN - 1][j][1]) << 16);
-      o.y = f32_to_bf16_rne(acc[TN - 1][j][2]) | (f32_to_bf16_rne(acc[TN - 1][j][3]) << 16);
+      o.x = pack(acc[TN - 1][j][0], acc[TN - 1][j][1]);
+      o.y = pack(acc[TN - 1][j][2], acc[TN - 1][j][3]);
       *reinterpret_cast<uint2*>(crow + col) = o;
     }
   }
@@ -585,7 +591,7 @@ void gemm_kernel(GemmArgs p) {
     const int64_t row = m0 + WM * wm + 16 * j + l16;
     if (row >= M) continue;
     if (MODE != kWgrad) {
-      store_row_bf16<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
+      store_row_bf16<VAR, TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       continue;
     }
 #pragma unroll
@@ -1357,7 +1363,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       } else if constexpr (VAR == kEpi) {
         store_row_epi<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       } else if (MODE != kWgrad) {
-        store_row_bf16<TN, TM>(p, acc, j, row, n0 + WN * wn, g);
+        store_row_bf16<VAR, TN, TM>(p, acc, j, row, n0 + WN * wn, g);
       } else {
 #pragma unroll
         for (int i = 0; i < TN; ++i) {
