@@ -472,8 +472,10 @@ def fp8bs_moe_combine(y, slot_rows, gates, out=None, stream=None):
     return out
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: a torch.cuda.Stream object costs 2 us
-_current_device = torch._C._cuda_getDevice
+# The handle alone, where torch offers it (these names are not published): a torch.cuda.Stream object costs 2 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _Tensor, _bf16, _f32, _u8, _i32 = torch.Tensor, torch.bfloat16, torch.float32, torch.uint8, torch.int32
 
 
