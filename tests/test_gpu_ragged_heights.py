@@ -1,10 +1,10 @@
-"""Every tile height of fp8bs_grouped_gemm_ragged: what a value that is not a number may reach."""
+"""Every tile height of fp8bs_grouped_gemm_ragged: long contractions, and what a value that is not a number may reach."""
 
 import numpy as np
 import pytest
 import torch
 
-from tests.linear_util import blocks, row_tiles
+from tests.linear_util import blocks, check, product64, row_tiles
 from tests.ragged_rules import CUS, grouped_tile_rows
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +62,24 @@ def test_not_a_number_stays_one(gpu_lib, experts, low, high, n, height, b_layout
     got, clean = got.cpu(), clean.cpu()
     assert torch.equal(torch.isnan(got), want)
     assert torch.equal(got[~want].view(torch.int16), clean[~want].view(torch.int16))
+
+
+@pytest.mark.parametrize("b_layout", [0, 1])
+@pytest.mark.parametrize("experts,low,high,n,height", HEIGHTS)
+def test_long_contractions(gpu_lib, experts, low, high, n, height, b_layout):
+    """13 blocks: every stage of a ring is refilled several times, the row scales are fetched for four blocks at a
+    time into both their buffers, and the last fetch is for one block."""
+    k = 13 * 128
+    lengths, seg = segments(experts, low, high)
+    rows = int(seg[-1])
+    assert not on_cus() or grouped_tile_rows(rows, experts, n, b_layout) == height
+    qa, sa, qb, sb = operands(3 * high + b_layout, rows, experts, n, k, b_layout)
+    c = torch.full((rows + 2, n + 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    gpu_lib.fp8bs_grouped_gemm_ragged(qa, sa, seg.cuda(), qb, sb, b_layout=b_layout, c=c[:rows, :n])
+    torch.cuda.synchronize()
+    assert (c[rows:] == 9.0).all() and (c[:, n:] == 9.0).all()
+    for i, length in enumerate(lengths):
+        cut = slice(int(seg[i]), int(seg[i + 1]))
+        if length:
+            y, err = product64(qa[cut], sa[cut], qb[i], sb[i], b_layout)
+            check(c[cut, :n], y.cpu(), err.cpu(), f"expert {i}, {length} rows")
