@@ -1,5 +1,6 @@
 """The host rules by which the ragged operators choose a tile height or a number of parts, restated for 256 CUs,
-so that a test can say which kernel its sizes reach.  fp8bs_grouped_gemm_ragged: skinny_cost and ragged_tile_rows."""
+so that a test can say which kernel its sizes reach.  fp8bs_grouped_gemm_ragged: skinny_cost and ragged_tile_rows;
+fp8bs_grouped_wgrad_ragged: wgrad_splits."""
 
 import math
 
@@ -36,3 +37,12 @@ def grouped_tile_rows(rows, experts, n, b_layout):
         if cost < best_cost:
             best, best_cost = bm, cost
     return best
+
+
+def wgrad_parts(rows, experts, m, n):
+    """Parts into which fp8bs_grouped_wgrad_ragged splits the rows (wgrad_splits), 1: not split."""
+    tiles = experts * -(-m // 256) * -(-n // 128)
+    slabs = rows // (experts * 64)
+    if 2 * tiles > CUS or slabs < 48:
+        return 1
+    return min(CUS // tiles, slabs // 8, 32)
