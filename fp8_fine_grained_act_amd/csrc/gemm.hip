@@ -912,6 +912,12 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
                 "tile shape");
   static_assert(VAR == kPlain || ((MODE == kFprop || MODE == kDgrad) && !SPLIT && !(VAR == kRagged && PERSIST)),
                 "variants of the bf16-output products");
+  // The plain dgrad on 192-row tiles writes its row indexes and copy counts out as
+  // a tile's rows and a constant, not from ra0 and jobs(): the same values, which
+  // the compiler schedules better there (1500 x 4096 x 4096 28.4 -> 28.0 us, 3000 x
+  // 2048 x 2048 16.8 -> 16.6, timed in turn) and worse elsewhere (grouped GEMM from
+  // bf16 weights 3.87 -> 3.90 ms, dgrad on 256-row tiles 30.3 -> 30.7 us).
+  constexpr bool kByRow = VAR == kPlain && MODE == kDgrad && BM == 192;
   static_assert(WAVES_M * WAVES_N == MW && WM % 16 == 0, "whole MFMA tiles per wave");
   static_assert(!W16 || (MODE == kGrouped && !PERSIST && !SPLIT && BM == 128 && BN == 256 && MW == 8),
                 "bf16 weights: grouped 128 x 256 tiles");
@@ -1057,7 +1063,9 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     // ragged: copy q = c + 4i covers 16 rows, 4 slabs' scales each (past the
     // last slab: scales of the next row, not used)
     const uint32_t voff_sa4 = (uint32_t)((16 * c + (lane >> 2)) * nkb + (lane & 3)) * 4u;
+    const int my_jobs = A_CP + B_CP + (c < SA_JOBS ? 1 : 0) + (c < SB_JOBS ? 1 : 0);
     auto jobs = [&](int kb) {
+      if (kByRow) return my_jobs;
       return A_CP + B_CP + (VAR == kRagged ? (kb % 4 == 0 ? BM / 64 : 0) : (c < SA_JOBS ? 1 : 0)) + (c < SB_JOBS ? 1 : 0);
     };
     auto issue = [&](int kb, Stage<BM, BN>& s) {
@@ -1191,20 +1199,21 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     float wbs[TN];  // or one per 16-column MFMA tile (kWbPerTile)
     v4f wb[TN];     // weight gradient: a scale per column
   };
-  // reads in the order of first use: B fragment 0 and A fragment 0 (the
-  // first MFMA), the scales (its fold), then the other B fragments
-  // row scales of this wave's rows in slab kb: ra0's, then one every kScaleStep
+  // the row scale of this wave's group t in slab kb
   constexpr int kScaleStep = (VAR == kRagged ? 4 : 1) * kGroupRows;
   auto row_scales = [&](const Stage<BM, BN>& s, int kb) -> const float* {
-    return VAR == kRagged ? &sa4[(kb >> 2) & 1][4 * ra0 + (kb & 3)] : &s.sa[ra0];
+    return VAR == kRagged ? &sa4[(kb >> 2) & 1][4 * ra0 + (kb & 3)] : kByRow ? s.sa : &s.sa[ra0];
   };
+  auto row_scale = [&](const float* sap, int t) { return sap[kByRow ? WM * wm + 16 * t + l16 : kScaleStep * t]; };
+  // reads in the order of first use: B fragment 0 and A fragment 0 (the
+  // first MFMA), the scales (its fold), then the other B fragments
   auto read_head = [&](const Stage<BM, BN>& s, const float* sap) {
     Head h;
     h.bf[0] = MODE == kDgrad ? frag_b_tr(s.b, 0) : frag(s.b, b_lo, b_hi, 0);
     h.a0 = frag_a(s.a, 0);
-    h.wa0 = sap[0];
+    h.wa0 = row_scale(sap, 0);
     h.a1 = frag_a(s.a, TM > 1 ? 1 : 0);
-    h.wa1 = sap[TM > 1 ? kScaleStep : 0];
+    h.wa1 = row_scale(sap, TM > 1 ? 1 : 0);
     if (MODE == kWgrad) {
 #pragma unroll
       for (int i = 0; i < TN; ++i) h.wb[i] = *reinterpret_cast<const v4f*>(&s.sb[WN * wn + 16 * i + 4 * g]);
@@ -1287,15 +1296,15 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       float wa_n2 = wa_n1;
       if (j + 2 < GR) {
         a_n2 = frag_a(s.a, j + 2);
-        wa_n2 = sap[kScaleStep * (j + 2)];
+        wa_n2 = row_scale(sap, j + 2);
       } else if (last && kEarly) {
         __builtin_amdgcn_s_waitcnt(0xC07F);    // lgkmcnt(0): slab kb fully read
         barrier();
         na0 = frag_a(sn.a, 0);
-        nwa0 = row_scales(sn, kb + 1)[0];
+        nwa0 = row_scale(row_scales(sn, kb + 1), 0);
         nwb0 = (MODE == kWgrad || kWbPerTile) ? 0.f : sn.sb[WN * wn];
         na1 = frag_a(sn.a, TM > 1 ? 1 : 0);
-        nwa1 = row_scales(sn, kb + 1)[TM > 1 ? kScaleStep : 0];
+        nwa1 = row_scale(row_scales(sn, kb + 1), TM > 1 ? 1 : 0);
       }
       const float wj = MODE == kWgrad ? wa_cur : wa_cur * hd.wb0;
 #pragma unroll
@@ -1350,7 +1359,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     const int64_t m0 = org.m0, n0 = org.n0;
 #pragma unroll
     for (int j = 0; j < decltype(groups)::value; ++j) {
-      const int64_t row = m0 + ra0 + kGroupRows * j;
+      const int64_t row = kByRow ? m0 + WM * wm + 16 * j + l16 : m0 + ra0 + kGroupRows * j;
       if (row >= M) continue;
       if (SPLIT) {
         float* prow = p.ws + ((int64_t)blockIdx.y * M + row) * N;
