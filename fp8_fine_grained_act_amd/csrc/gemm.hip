@@ -230,6 +230,20 @@ struct GemmCfg {
   }
 };
 
+// Two tiles' values of one row (4 columns each) rounded to bf16 and stored as the
+// 16-byte piece described at store_row_bf16.
+__device__ __forceinline__ void store_pair(uint16_t* dst, const float (&x)[4], const float (&y)[4], int stream_out) {
+  const uint32_t x0 = pack_bf16(x[0], x[1]), x1 = pack_bf16(x[2], x[3]);
+  const uint32_t y0 = pack_bf16(y[0], y[1]), y1 = pack_bf16(y[2], y[3]);
+  const auto s0 = __builtin_amdgcn_permlane16_swap(x0, y0, false, false);
+  const auto s1 = __builtin_amdgcn_permlane16_swap(x1, y1, false, false);
+  const uint4 v = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+  if (stream_out)
+    store_nt(dst, v);
+  else
+    *reinterpret_cast<uint4*>(dst) = v;
+}
+
 // bf16 output of one 16-row MFMA group.  The MFMA leaves lane (g, r)
 // (g = lane / 16, r = lane % 16) with columns 4g..4g+3 of output row r of
 // each 16x16 tile, so storing a tile as it stands writes four 8-byte pieces
@@ -247,18 +261,6 @@ struct GemmCfg {
 // 4096x32768x512, 268 MB of bf16: 130 -> 116 us; the MoE grouped GEMM's 535 MB
 // row capacity 2.24 -> 2.18 ms; an output that fits, such as dgrad's
 // 4096x7168, was 5% slower with it).
-__device__ __forceinline__ void store_pair(uint16_t* dst, const float (&x)[4], const float (&y)[4], int stream_out) {
-  const uint32_t x0 = pack_bf16(x[0], x[1]), x1 = pack_bf16(x[2], x[3]);
-  const uint32_t y0 = pack_bf16(y[0], y[1]), y1 = pack_bf16(y[2], y[3]);
-  const auto s0 = __builtin_amdgcn_permlane16_swap(x0, y0, false, false);
-  const auto s1 = __builtin_amdgcn_permlane16_swap(x1, y1, false, false);
-  const uint4 v = make_uint4(s0[0], s1[0], s0[1], s1[1]);
-  if (stream_out)
-    store_nt(dst, v);
-  else
-    *reinterpret_cast<uint4*>(dst) = v;
-}
-
 // Ragged segments round in the hardware's conversion, as the few-row tiles do
 // (skinny.hip), so that a NaN stays one whatever tile its row falls into; finite
 // values and infinities round to the same bits either way.
@@ -1949,6 +1951,11 @@ static bool epi_on_128(int64_t m, int64_t n, bool fwd, int cus) {
   return tile_cost(m, n, 128, 128, 118, cus) < best;
 }
 
+// The contraction is not split over workgroups, as fp8bs_gemm does with a workspace:
+// 4 to 700 rows of n = 4096, k = 7168 with a bias take 8-31 us here (12-31 in layout
+// 1) against 27-37 us for the plain product, but few tiles over a very long
+// contraction take longer (4096 x 512 x 32768, 128 workgroups of 256 slabs: 121
+// against 79 us, 128 against 80 in layout 1).
 extern "C" int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb,
                                    int64_t m, int64_t n, int64_t k, int b_layout, const float* bias, int act,
                                    const uint16_t* residual, int64_t ldr, uint16_t* z, int64_t ldz, uint16_t* c,

@@ -4,13 +4,18 @@
 //
 // (the residual's gradient is dy itself).  dz goes on to the quantizers and the
 // dgrad and wgrad products.  One pass over dy and z, bound by HBM (6 bytes per
-// element): a workgroup owns a strip of columns and a run of rows, wave w
-// taking rows w, w + kBwdWaves, ...; each lane sums its 8 columns' FP32 dz in
-// registers, the waves' sums meet in LDS in wave order.  With one run of rows
-// the workgroup writes dbias itself; otherwise its sums go to the caller's
-// workspace [runs][n] and bias_sum_kernel adds the runs in order.  No atomics:
-// the bits depend on (m, n) only.  dbias sums the FP32 dz, before its bf16
-// rounding.
+// element): a workgroup owns a strip of columns and a run of rows, each lane sums
+// its 8 columns' FP32 dz in registers, the waves' sums meet in LDS in wave order.
+//   more than kNarrowRows rows: strips of 512 columns, a wave's 64 lanes on one
+//     row; wave w takes rows w, w + 8, ... of its run.  With one run of rows the
+//     workgroup writes dbias itself; otherwise its sums go to the caller's
+//     workspace [runs][n] and bias_sum_kernel adds the runs in order.
+//   up to kNarrowRows rows: strips of 64 columns, one run; 8 lanes on a row, a
+//     wave's step 8 rows (wave w rows 8 w .. 8 w + 7, then every 64th row from
+//     each), so a column's sums of 8 lanes are added across the wave first, lanes
+//     8, 16 and 32 apart in turn.
+// No atomics: the bits depend on (m, n) only.  dbias sums the FP32 dz, before its
+// bf16 rounding.
 //
 // About 512 workgroups of 8 waves with 2 rows each in flight: 16384 x 4096 with
 // GELU in 75 us, both launches (403 MB, 5.4 TB/s).  2048 workgroups of 4 waves with 4

@@ -6,11 +6,12 @@
  * returns at once.  The caller owns every buffer it passes.
  *
  * Memory and state:
- *   - Two calls allocate: fp8bs_gemm and fp8bs_gemm_wgrad, when they split
- *     the contraction over workgroups, take their FP32 partials from a
- *     stream-ordered allocation on the call's stream (hipMallocAsync, freed
- *     with hipFreeAsync after use).  If that allocation fails they clear the
- *     runtime's error and run the unsplit kernels instead.
+ *   - Three calls allocate: fp8bs_gemm, fp8bs_gemm_wgrad and
+ *     fp8bs_grouped_wgrad_ragged, when they split the contraction over
+ *     workgroups, take their FP32 partials from a stream-ordered allocation on
+ *     the call's stream (hipMallocAsync, freed with hipFreeAsync after use).  If
+ *     that allocation fails they clear the runtime's error and run the unsplit
+ *     kernels instead.
  *     fp8bs_gemm_noalloc is fp8bs_gemm without allocation.
  *   - The library caches one value per device: its compute-unit count (an
  *     atomic per device ordinal, filled on first use).  Tile shapes and the
@@ -442,7 +443,9 @@ int fp8bs_moe_combine(const uint16_t* y, int64_t ldy, int64_t rows_cap, const in
  *   z         bf16 [m, n], row stride ldz elements, or NULL; must not overlap c
  * ldr and ldz are ignored where their pointer is NULL.
  * Alignment: as for fp8bs_gemm; residual and z 16 bytes, ldr and ldz % 8 == 0,
- * bias 4 bytes.  Errors: FP8BS_ERR_FLAG for an unknown act.  Never allocates.
+ * bias 4 bytes.  Errors: FP8BS_ERR_FLAG for an unknown act.  Never allocates, and
+ * never splits the contraction over workgroups: where fp8bs_gemm does, with few
+ * output tiles over a very long contraction, it can be the faster of the two.
  */
 int fp8bs_gemm_epilogue(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t m,
                         int64_t n, int64_t k, int b_layout, const float* bias, int act,
