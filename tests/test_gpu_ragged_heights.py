@@ -64,12 +64,13 @@ def test_not_a_number_stays_one(gpu_lib, experts, low, high, n, height, b_layout
     assert torch.equal(got[~want].view(torch.int16), clean[~want].view(torch.int16))
 
 
+@pytest.mark.parametrize("blocks_k", [1, 2, 13])
 @pytest.mark.parametrize("b_layout", [0, 1])
 @pytest.mark.parametrize("experts,low,high,n,height", HEIGHTS)
-def test_long_contractions(gpu_lib, experts, low, high, n, height, b_layout):
+def test_short_and_long_contractions(gpu_lib, experts, low, high, n, height, b_layout, blocks_k):
     """13 blocks: every stage of a ring is refilled several times, the row scales are fetched for four blocks at a
-    time into both their buffers, and the last fetch is for one block."""
-    k = 13 * 128
+    time into both their buffers, and the last fetch is for one block.  1 and 2: the ring is not even filled."""
+    k = 128 * blocks_k
     lengths, seg = segments(experts, low, high)
     rows = int(seg[-1])
     assert not on_cus() or grouped_tile_rows(rows, experts, n, b_layout) == height

@@ -100,3 +100,32 @@ def test_two_graphs_replayed_at_once(gpu_lib):
         eager = [gpu_lib.fp8bs_grouped_wgrad_ragged(dy, x, seg_d) for (seg, dy, x), (_, seg_d) in zip(cases, graphs)]
         for out, w, again in zip(outs, want, eager):
             assert torch.equal(out, w) and torch.equal(again, w), i
+
+
+@pytest.mark.parametrize("rows", [40, 13000])
+def test_odd_offsets_and_strides_are_harmless(gpu_lib, rows):
+    """Offsets outside the rows are clipped and a backwards segment is empty, split or not; NaN in the columns between
+    the matrix and its row stride, and in rows of no segment, reach nothing."""
+    m, n = 72, 136
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    dy = torch.randint(-2, 3, (rows, m + 16), generator=g, device="cuda").bfloat16()
+    x = torch.randint(-2, 3, (rows, n + 8), generator=g, device="cuda").bfloat16()
+    dy[:, m:], x[:, n:] = float("nan"), float("inf")
+    seg = torch.tensor([-7, 10, 4, rows - 10, 1 << 29], dtype=torch.int32)
+    cuts = [slice(0, 10), None, slice(4, rows - 10), slice(rows - 10, rows)]
+    c = torch.full((5, m, n), 7.0, device="cuda")
+    gpu_lib.fp8bs_grouped_wgrad_ragged(dy[:, :m], x[:, :n], seg.cuda(), c=c[:4])
+    torch.cuda.synchronize()
+    assert (c[4] == 7.0).all() and (c[1] == 0.0).all()
+    for i, cut in enumerate(cuts):
+        if cut is not None:
+            assert torch.equal(c[i], (dy[cut, :m].double().t() @ x[cut, :n].double()).float()), i
+    # a segment that ends before the rows do: what lies behind is not read
+    seg = torch.tensor([5, 5, 5, rows - 9, rows - 9], dtype=torch.int32)
+    dy[:5], dy[rows - 9:], x[:5], x[rows - 9:] = (float("nan"),) * 4
+    gpu_lib.fp8bs_grouped_wgrad_ragged(dy[:, :m], x[:, :n], seg.cuda(), c=c[:4])
+    torch.cuda.synchronize()
+    assert (c[0] == 0.0).all() and (c[1] == 0.0).all() and (c[3] == 0.0).all()
+    cut = slice(5, rows - 9)
+    assert torch.equal(c[2], (dy[cut, :m].double().t() @ x[cut, :n].double()).float())
