@@ -1592,8 +1592,8 @@ using namespace fp8bs;
 // keeps more of the chip busy.  Counting 256 x 128 tiles against three
 // quarters of the CUs, as before the 192-row tiles existed, sent shapes the
 // warp-specialized kernel runs 18-41% faster to gemm_kernel (1536x3584 weight
-// gradient over 16384 tokens: 188 -> 110 us; forward 3072x1536x7168: 55.7 ->
-// 41.6 us); below a quarter (forward) it loses (768x2048x7168: 35.6 -> 38.9 us).
+// gradient over 16384 tokens: 188 -> 110 us; forward 2048x2048x2048: 16.8 ->
+// 14.1 us); below a quarter (forward) it loses (768x2048x7168: 35.6 -> 38.9 us).
 static bool use_ws(int64_t m, int64_t n, bool wgrad) {
   const int64_t tiles = ((m + 191) / 192) * ((n + 127) / 128);
   return (wgrad ? 4 : 2) * tiles >= cu_count();
