@@ -7,7 +7,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8bs.so")
-SOURCES = ["quantize.hip", "requant.hip", "gemm.hip", "skinny.hip", "moe.hip", "linear_bwd.hip", "wgrad_ragged.hip"]
+SOURCES = ["quantize.hip", "requant.hip", "gemm.hip", "skinny.hip", "moe.hip", "linear_bwd.hip", "wgrad_ragged.hip",
+           "gated.hip", "adamw.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -56,6 +56,22 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return v;
 }
 
+// max of non-negative floats (they order as their bits) over aligned groups of 16
+// lanes, and with the lane 16 or 32 away (a swap of the operand with itself leaves
+// both lanes' values in each)
+__device__ __forceinline__ float max16_f32(float v) {
+  const uint32_t m = max8_u32(__float_as_uint(v));
+  return __uint_as_float(max(m, dpp_shuffle<0x140>(m)));
+}
+__device__ __forceinline__ float max_xor16_f32(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(max(s[0], s[1]));
+}
+__device__ __forceinline__ float max_xor32_f32(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(max(s[0], s[1]));
+}
+
 // lane-wise max of two pairs of 16-bit unsigned values (one v_pk_max_u16)
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -140,6 +156,38 @@ __device__ __forceinline__ void quant_run(const uint32_t* in, uint32_t* out, con
   }
 }
 
+// Groups of FP32 values that never were bf16 (a gated product, a gradient, an
+// optimizer state): s = amax / 448 and codes of x / s as above.  x / s takes the
+// same two operations, fma(x, r, x * rl): r + rl is 1 / s to about 2^-48, so the
+// result is the correctly rounded quotient but where that lies within 2^-47 of a
+// midpoint of two FP32 values.  For amax below 2^-64 both sides are scaled by 2^64
+// (s may be subnormal); such an s carries fewer bits, so the quotient is clipped to
+// 448 there (elsewhere it stays below 448 (1 + 2^-22), which codes as 448).  Where s
+// underflows to zero (amax < 2^-141) the codes are signed zeros.
+struct F32Scale {
+  float s, r, rl, up;
+};
+__device__ __forceinline__ F32Scale f32_scale(float amax) {
+  F32Scale g;
+  g.s = amax / kE4M3Max;
+  g.up = amax < 0x1p-64f ? kTinyScale : 1.0f;
+  const float d = g.s * g.up;
+  g.r = d == 0.0f ? 0.0f : 1.0f / d;
+  g.rl = __builtin_fmaf(-d, g.r, 1.0f) * g.r;
+  return g;
+}
+// SLOW: some group of the wave is that small.
+template <bool SLOW>
+__device__ __forceinline__ float f32_quotient(float x, const F32Scale& g) {
+  if (!SLOW) return __builtin_fmaf(x, g.r, x * g.rl);
+  const float v = x * g.up;
+  return __builtin_amdgcn_fmed3f(__builtin_fmaf(v, g.r, v * g.rl), -kE4M3Max, kE4M3Max);
+}
+__device__ __forceinline__ uint32_t code4_f32(float a, float b, float c, float d) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
+}
+
 // fp32 -> bf16 bits, round to nearest even (finite inputs)
 __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   uint32_t u = __float_as_uint(f);
@@ -215,6 +263,27 @@ __device__ __forceinline__ float act_slope(float z) {
     return __builtin_fmaf(z * p, 1.0f - p, p);
   }
   return 1.0f;
+}
+
+// act(z) and act'(z) from one sigma.
+template <int ACT>
+__device__ __forceinline__ void act_both(float z, float& a, float& slope) {
+  if (ACT == FP8BS_ACT_RELU) {
+    a = z < 0.0f ? 0.0f : z;
+    slope = z > 0.0f ? 1.0f : 0.0f;
+  } else if (ACT == FP8BS_ACT_GELU_TANH) {
+    const float c = z == z ? gelu_clip(z) : z, cc = c * c;
+    const float p = sigmoid_of(c * __builtin_fmaf(kGeluC1, cc, kGeluC0));
+    a = z * p;
+    slope = __builtin_fmaf(c * p * (1.0f - p), __builtin_fmaf(3.0f * kGeluC1, cc, kGeluC0), p);
+  } else if (ACT == FP8BS_ACT_SILU) {
+    const float p = sigmoid_of(z);
+    a = z * p;
+    slope = __builtin_fmaf(a, 1.0f - p, p);
+  } else {
+    a = z;
+    slope = 1.0f;
+  }
 }
 
 // ---- streaming (non-temporal) 16-byte loads and stores ----------------------

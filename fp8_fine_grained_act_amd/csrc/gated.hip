@@ -1,0 +1,376 @@
+// A gated feed-forward block, h = act(x Wg^T) * (x Wu^T): the entry points of its
+// forward pass and the kernels of its backward pass.
+//
+// Backward, element by element from dh and the kept z = [g, u] (bf16):
+//   dg = dh * u * act'(g),   du = dh * act(g),   h = act(g) * u
+// with act(g) and act'(g) from one sigma (common.h).  What the products of the
+// backward pass read is made in the same pass, from the unrounded FP32 values: the
+// 1x128 tiles of dz = [dg, du] along the columns (activation gradient), and along the
+// rows, transposed (weight gradients of both weights; h's for the down projection).
+// Bound by HBM: 6 bytes read per element of h, 2 to 10 written.
+
+#include "common.h"
+#include "gated.h"
+#include "launch.h"
+
+namespace fp8bs {
+
+// ---- codes of h from its FP32 values -----------------------------------------------
+// h [m, n] FP32 contiguous -> 1x128 tiles along the columns.  16 lanes per tile, 8 values each.  With
+// seg only the rows of segments (between the first offset and the last).
+__global__ __launch_bounds__(256) void quant_h_kernel(const float* __restrict__ hf, int64_t m, int64_t n,
+                                                      const int32_t* __restrict__ seg, int64_t num_experts,
+                                                      uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
+  const int lane16 = threadIdx.x & 15;
+  const uint32_t tiles_n = (uint32_t)(n / kGroup);
+  const uint32_t t = blockIdx.x * 16u + (threadIdx.x >> 4);
+  const int64_t row = t / tiles_n, tb = t - (uint32_t)row * tiles_n;
+  if (row >= m) return;                        // the 16 lanes of a tile together
+  if (seg && (row < seg[0] || row >= seg[num_experts])) return;
+  const float4* const src = reinterpret_cast<const float4*>(hf + row * n + tb * kGroup + 8 * lane16);
+  const float4 a = src[0], b = src[1];
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+  const F32Scale g = f32_scale(max16_f32(top));
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = f32_quotient<true>(x[i], g);
+  *reinterpret_cast<uint2*>(q + row * ldq + tb * kGroup + 8 * lane16) =
+      make_uint2(code4_f32(v[0], v[1], v[2], v[3]), code4_f32(v[4], v[5], v[6], v[7]));
+  if (lane16 == 0) s[t] = g.s;
+}
+
+static int quant_h(const GatedArgs& a, hipStream_t s) {
+  const int64_t tiles = a.p.m * (a.p.n / kGroup);
+  hipLaunchKernelGGL(quant_h_kernel, dim3((unsigned)((tiles + 15) / 16)), dim3(256), 0, s, a.p.hf, a.p.m, a.p.n, a.p.seg,
+                     a.p.num_experts, a.qh, a.ldqh, a.sh);
+  return launch_status();
+}
+
+// ---- backward ----------------------------------------------------------------------
+struct GatedBwdArgs {
+  const uint16_t* dh;
+  int64_t lddh;
+  const uint16_t* z;
+  int64_t ldz;
+  int64_t m, n;
+  uint16_t* dz;              // [m, 2n] or null
+  int64_t lddz;
+  uint8_t* q;                // [m, 2n] or null
+  int64_t ldq;
+  float* s;                  // [m, 2n/128]
+  uint8_t* qt;               // [2n, m] or null
+  int64_t ldqt;
+  float* st;                 // [2n, m/128]
+  uint16_t* h;               // [m, n] or null
+  int64_t ldh;
+  uint8_t* qht;              // [n, m] or null
+  int64_t ldqht;
+  float* sht;                // [n, m/128]
+  const int32_t* row_end;    // rows from *row_end on are left alone, or null
+};
+
+// 8 columns of one row: dg, du and h from the packed bf16 inputs
+template <int ACT>
+__device__ __forceinline__ void gated_slopes(uint4 dh, uint4 g, uint4 u, float (&dg)[8], float (&du)[8], float (&h)[8]) {
+  const uint32_t d4[4] = {dh.x, dh.y, dh.z, dh.w}, g4[4] = {g.x, g.y, g.z, g.w}, u4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = i & 1 ? bf16_hi(d4[i / 2]) : bf16_lo(d4[i / 2]);
+    const float gv = i & 1 ? bf16_hi(g4[i / 2]) : bf16_lo(g4[i / 2]);
+    const float uv = i & 1 ? bf16_hi(u4[i / 2]) : bf16_lo(u4[i / 2]);
+    float a, slope;
+    act_both<ACT>(gv, a, slope);
+    dg[i] = d * uv * slope;
+    du[i] = d * a;
+    h[i] = a * uv;
+  }
+}
+
+__device__ __forceinline__ float top8(const float (&x)[8]) {
+  float t = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t = fmaxf(t, fabsf(x[i]));
+  return t;
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// 8 codes of one row's tile piece, its scale stored by the tile's first lane (16 lanes a tile)
+__device__ __forceinline__ void store_row_codes(const float (&x)[8], uint8_t* q, float* s, int lane16) {
+  const F32Scale g = f32_scale(max16_f32(top8(x)));
+  float v[8];
+  if (__ballot(g.up != 1.0f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f32_quotient<true>(x[i], g);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f32_quotient<false>(x[i], g);
+  }
+  *reinterpret_cast<uint2*>(q) = make_uint2(code4_f32(v[0], v[1], v[2], v[3]), code4_f32(v[4], v[5], v[6], v[7]));
+  if (lane16 == 0) *s = g.s;
+}
+
+// Without transposed outputs: 16 lanes per piece of 128 columns of a row.
+template <int ACT, bool STREAM>
+__global__ __launch_bounds__(256) void gated_bwd_rows_kernel(GatedBwdArgs p, uint32_t pieces_n, uint32_t pieces) {
+  const int lane16 = threadIdx.x & 15;
+  const uint32_t t = blockIdx.x * 16u + (threadIdx.x >> 4);
+  if (t >= pieces) return;
+  const uint32_t row = t / pieces_n, tb = t - row * pieces_n;
+  const int64_t col = (int64_t)tb * kGroup + 8 * lane16;
+  if (col >= p.n || (p.row_end && (int64_t)row >= *p.row_end)) return;   // n % 128 != 0 has no codes: no lane is waited for
+  auto load = [](const uint16_t* a) { return STREAM ? load_nt(a) : *reinterpret_cast<const uint4*>(a); };
+  auto store = [](uint16_t* a, uint4 v) {
+    if (STREAM) store_nt(a, v);
+    else *reinterpret_cast<uint4*>(a) = v;
+  };
+  const uint16_t* const zr = p.z + row * p.ldz + col;
+  const uint4 dhv = load(p.dh + row * p.lddh + col), gv = load(zr), uv = load(zr + p.n);
+  float dg[8], du[8], h[8];
+  gated_slopes<ACT>(dhv, gv, uv, dg, du, h);
+  if (p.dz) {
+    store(p.dz + row * p.lddz + col, pack8(dg));
+    store(p.dz + row * p.lddz + p.n + col, pack8(du));
+  }
+  if (p.h) store(p.h + row * p.ldh + col, pack8(h));
+  if (p.q) {
+    uint8_t* const qr = p.q + row * p.ldq + col;
+    float* const sr = p.s + row * (int64_t)(2 * pieces_n) + tb;
+    store_row_codes(dg, qr, sr, lane16);
+    store_row_codes(du, qr + p.n, sr + pieces_n, lane16);
+  }
+}
+
+// With transposed outputs: a workgroup of 8 waves owns a square of 128 rows and 128
+// columns of h.  Thread (cg, rg) = (tid % 16, tid / 16) holds columns 8 cg .. 8 cg + 7 of rows
+// 4 rg .. 4 rg + 3 in FP32 registers, so both tile directions are coded from the
+// same values without staging them: a row's amax crosses its 16 lanes (DPP), a
+// column's the wave (two lane swaps) and then the waves in LDS.  The transposed
+// codes, 4 bytes of a column per thread, meet in LDS and leave as whole 128-byte
+// rows of the output: dword d of column c is stored at d ^ (4 * ((c / 8) % 8)), which
+// keeps 16-byte chunks whole and puts a wave's 64 writes on 32 banks, two each.
+template <int ACT, bool STREAM>
+__global__ __launch_bounds__(512) void gated_bwd_square_kernel(GatedBwdArgs p) {
+  __shared__ float tops[3][8][128];            // [dg, du, h][wave][column]
+  __shared__ float4 scl[3][128];               // a column's r, rl, up
+  __shared__ __attribute__((aligned(16))) uint32_t codes[3][128 * 32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int cg = tid & 15, rg = tid >> 4;
+  const int64_t c0 = (int64_t)blockIdx.x * 128, r0 = (int64_t)blockIdx.y * 128;
+  const int64_t col = c0 + 8 * cg;
+  const int nq = p.qht ? 3 : 2, q0 = p.qt ? 0 : 2;
+  auto load = [](const uint16_t* a) { return STREAM ? load_nt(a) : *reinterpret_cast<const uint4*>(a); };
+  uint4 dhv[4], gv[4], uv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = r0 + 4 * rg + i;
+    dhv[i] = load(p.dh + row * p.lddh + col);
+    gv[i] = load(p.z + row * p.ldz + col);
+    uv[i] = load(p.z + row * p.ldz + p.n + col);
+  }
+  float x[3][4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    gated_slopes<ACT>(dhv[i], gv[i], uv[i], x[0][i], x[1][i], x[2][i]);
+    const int64_t row = r0 + 4 * rg + i;
+    if (p.dz) {
+      *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = pack8(x[0][i]);
+      *reinterpret_cast<uint4*>(p.dz + row * p.lddz + p.n + col) = pack8(x[1][i]);
+    }
+    if (p.h) *reinterpret_cast<uint4*>(p.h + row * p.ldh + col) = pack8(x[2][i]);
+    if (p.q) {
+      uint8_t* const qr = p.q + row * p.ldq + col;
+      float* const sr = p.s + row * (2 * p.n / kGroup) + blockIdx.x;
+      store_row_codes(x[0][i], qr, sr, cg);
+      store_row_codes(x[1][i], qr + p.n, sr + p.n / kGroup, cg);
+    }
+  }
+  // columns' maxima
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      t[j] = fmaxf(fmaxf(fabsf(x[q][0][j]), fabsf(x[q][1][j])), fmaxf(fabsf(x[q][2][j]), fabsf(x[q][3][j])));
+      t[j] = max_xor16_f32(t[j]);
+      t[j] = max_xor32_f32(t[j]);
+    }
+    if (lane < 16) {
+      *reinterpret_cast<float4*>(&tops[q][wave][8 * cg]) = make_float4(t[0], t[1], t[2], t[3]);
+      *reinterpret_cast<float4*>(&tops[q][wave][8 * cg + 4]) = make_float4(t[4], t[5], t[6], t[7]);
+    }
+  }
+  __syncthreads();
+  if (tid < 384) {
+    const int q = tid >> 7, c = tid & 127;
+    float t = tops[q][0][c];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t = fmaxf(t, tops[q][w][c]);
+    const F32Scale g = f32_scale(t);
+    scl[q][c] = make_float4(g.r, g.rl, g.up, 0.0f);
+    if (q >= q0 && q < nq) {
+      float* const s = q == 2 ? p.sht : p.st + (q * p.n) * (p.m / kGroup);
+      s[(c0 + c) * (p.m / kGroup) + blockIdx.y] = g.s;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    if (q < q0 || q >= nq) continue;
+    F32Scale g[8];
+    bool tiny = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 v = scl[q][8 * cg + j];
+      g[j] = F32Scale{0.0f, v.x, v.y, v.z};
+      tiny = tiny || v.z != 1.0f;
+    }
+    const bool slow = __ballot(tiny) != 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = slow ? f32_quotient<true>(x[q][i][j], g[j]) : f32_quotient<false>(x[q][i][j], g[j]);
+      codes[q][(8 * cg + j) * 32 + (rg ^ ((cg & 7) << 2))] = code4_f32(v[0], v[1], v[2], v[3]);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    if (q < q0 || q >= nq) continue;
+    uint8_t* const out = q == 2 ? p.qht : p.qt + q * p.n * p.ldqt;
+    const int64_t ld = q == 2 ? p.ldqht : p.ldqt;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = 64 * i + (tid >> 3), k = tid & 7;
+      const uint4 v = *reinterpret_cast<const uint4*>(&codes[q][c * 32 + 4 * (k ^ ((c >> 3) & 7))]);
+      *reinterpret_cast<uint4*>(out + (c0 + c) * ld + r0 + 16 * k) = v;
+    }
+  }
+}
+
+template <int ACT>
+static int launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s) {
+  const bool stream = 6 * a.m * a.n > kStreamBytes;
+  if (a.qt || a.qht) {
+    const dim3 grid((unsigned)(a.n / kGroup), (unsigned)(a.m / kGroup));
+    if (stream) hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, true>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, false>), grid, dim3(512), 0, s, a);
+    return launch_status();
+  }
+  const int64_t pieces_n = (a.n + kGroup - 1) / kGroup, pieces = a.m * pieces_n;
+  const dim3 grid((unsigned)((pieces + 15) / 16));
+  if (stream) hipLaunchKernelGGL((gated_bwd_rows_kernel<ACT, true>), grid, dim3(256), 0, s, a, (uint32_t)pieces_n, (uint32_t)pieces);
+  else hipLaunchKernelGGL((gated_bwd_rows_kernel<ACT, false>), grid, dim3(256), 0, s, a, (uint32_t)pieces_n, (uint32_t)pieces);
+  return launch_status();
+}
+
+}  // namespace fp8bs
+
+using namespace fp8bs;
+
+static bool fits_u32(int64_t bytes) { return bytes < 0xFFFFFFFFLL; }
+
+// Checks shared by the two forward entry points (m, n, k known to be non-negative).
+static int gated_check(const GatedArgs& a, float* workspace) {
+  const SkinnyArgs& p = a.p;
+  if ((a.qh == nullptr) != (a.sh == nullptr) || (p.m > 0 && !p.c && !a.qh)) return FP8BS_ERR_NULL;
+  if (p.epi.act < FP8BS_ACT_NONE || p.epi.act > FP8BS_ACT_SILU) return FP8BS_ERR_FLAG;
+  if (p.n <= 0 || p.k <= 0 || p.n % 128 || p.k % BK || (p.c && p.ldc < p.n) || (p.epi.z && p.epi.ldz < 2 * p.n) ||
+      (a.qh && a.ldqh < p.n) || p.n > 0x3FFFFFFFLL || !fits_u32(256 * p.k) || p.n > 0xFFFFFFFFLL / (2 * p.k) ||
+      p.m > kMaxGrid / (p.n / 16))
+    return FP8BS_ERR_SHAPE;
+  if (!aligned(p.qa, 16) || !aligned(p.qb, 16) || !aligned(p.sa, 4) || !aligned(p.sb, 4) || !aligned(p.seg, 4) ||
+      (p.c && (!aligned(p.c, 16) || p.ldc % 8)) || (p.epi.z && (!aligned(p.epi.z, 16) || p.epi.ldz % 8)) ||
+      (a.qh && (!aligned(a.qh, 16) || a.ldqh % 16 || !aligned(a.sh, 4))) || !aligned(workspace, 16))
+    return FP8BS_ERR_ALIGN;
+  return FP8BS_OK;
+}
+
+static int64_t gated_workspace(const GatedArgs& a) { return a.qh ? 4 * a.p.m * a.p.n : 0; }
+
+static int gated_run(GatedArgs a, float* workspace, int64_t workspace_bytes, hipStream_t s) {
+  const int64_t need = gated_workspace(a);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP8BS_ERR_SCRATCH;
+  a.p.hf = need > 0 ? workspace : nullptr;
+  int st = launch_skinny(a.p, 0, cu_count(), s);
+  if (st == FP8BS_OK && a.qh) st = quant_h(a, s);
+  return st;
+}
+
+extern "C" int64_t fp8bs_gemm_gated_workspace(int64_t m, int64_t n, int64_t k) {
+  GatedArgs a{};
+  if (m <= 0 || k <= 0) return FP8BS_ERR_SHAPE;
+  a.p.m = m;
+  a.p.n = n;
+  a.p.k = k;
+  a.p.gated = 1;
+  a.p.num_experts = 1;
+  a.qh = reinterpret_cast<uint8_t*>(16);
+  a.sh = reinterpret_cast<float*>(16);
+  a.ldqh = n > 0 ? (n + 15) / 16 * 16 : 0;
+  const int st = gated_check(a, nullptr);
+  return st == FP8BS_OK ? gated_workspace(a) : st;
+}
+
+extern "C" int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t total_rows, int64_t n, int64_t k) {
+  if (num_experts < 1 || num_experts > 65536 || total_rows < 0 || total_rows > 0x3FFFFFFFLL) return FP8BS_ERR_SHAPE;
+  return total_rows == 0 ? 0 : fp8bs_gemm_gated_workspace(total_rows, n, k);
+}
+
+extern "C" int fp8bs_gemm_gated(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t m, int64_t n,
+                                int64_t k, int act, uint16_t* z, int64_t ldz, uint16_t* h, int64_t ldh, uint8_t* qh,
+                                int64_t ldqh, float* sh, float* workspace, int64_t workspace_bytes, void* stream) {
+  if (!qa || !sa || !qb || !sb) return FP8BS_ERR_NULL;
+  if (m <= 0 || k <= 0) return FP8BS_ERR_SHAPE;
+  GatedArgs a{{qa, sa, qb, sb, h, ldh, m, n, k, nullptr, 1, Epilogue{nullptr, nullptr, 0, z, ldz, act}, 1, nullptr}, qh, ldqh, sh};
+  const int chk = gated_check(a, workspace);
+  return chk != FP8BS_OK ? chk : gated_run(a, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+extern "C" int fp8bs_grouped_gemm_gated_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets,
+                                               int64_t num_experts, int64_t total_rows, const uint8_t* qb, const float* sb,
+                                               int64_t n, int64_t k, int act, uint16_t* z, int64_t ldz, uint16_t* h,
+                                               int64_t ldh, uint8_t* qh, int64_t ldqh, float* sh, float* workspace,
+                                               int64_t workspace_bytes, void* stream) {
+  if (!seg_offsets || !qb || !sb || (total_rows > 0 && (!qa || !sa))) return FP8BS_ERR_NULL;
+  if (num_experts < 1 || num_experts > 65536 || total_rows < 0 || total_rows > 0x3FFFFFFFLL || k <= 0) return FP8BS_ERR_SHAPE;
+  GatedArgs a{{qa, sa, qb, sb, h, ldh, total_rows, n, k, seg_offsets, num_experts, Epilogue{nullptr, nullptr, 0, z, ldz, act},
+               1, nullptr}, qh, ldqh, sh};
+  const int chk = gated_check(a, workspace);
+  if (chk != FP8BS_OK || total_rows == 0) return chk;
+  return gated_run(a, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+extern "C" int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int64_t ldz, int64_t m, int64_t n,
+                                    int act, uint16_t* dz, int64_t lddz, uint8_t* q, int64_t ldq, float* scales, uint8_t* qt,
+                                    int64_t ldqt, float* scales_t, uint16_t* h, int64_t ldh, uint8_t* qht, int64_t ldqht,
+                                    float* scales_ht, const int32_t* row_end, void* stream) {
+  if (!dh || !z || (!dz && !q && !qt && !h && !qht) || (q == nullptr) != (scales == nullptr) ||
+      (qt == nullptr) != (scales_t == nullptr) || (qht == nullptr) != (scales_ht == nullptr))
+    return FP8BS_ERR_NULL;
+  if (act < FP8BS_ACT_NONE || act > FP8BS_ACT_SILU) return FP8BS_ERR_FLAG;
+  const bool cols = qt || qht;
+  if (m <= 0 || n <= 0 || n % 8 || n > 0x3FFFFFFFLL || m > 0x7FFFFFFFLL || ((q || cols) && n % kGroup) ||
+      (cols && (m % kGroup || row_end || m / kGroup > 65535)) || m > kMaxGrid / ((n + kGroup - 1) / kGroup) - 16 || lddh < n ||
+      ldz < 2 * n || (dz && lddz < 2 * n) || (q && ldq < 2 * n) || (qt && ldqt < m) || (h && ldh < n) || (qht && ldqht < m))
+    return FP8BS_ERR_SHAPE;
+  if (!aligned(dh, 16) || lddh % 8 || !aligned(z, 16) || ldz % 8 || (dz && (!aligned(dz, 16) || lddz % 8)) ||
+      (q && (!aligned(q, 16) || ldq % 16)) || (qt && (!aligned(qt, 16) || ldqt % 16)) || (h && (!aligned(h, 16) || ldh % 8)) ||
+      (qht && (!aligned(qht, 16) || ldqht % 16)) || !aligned(scales, 4) || !aligned(scales_t, 4) || !aligned(scales_ht, 4) ||
+      !aligned(row_end, 4))
+    return FP8BS_ERR_ALIGN;
+  const GatedBwdArgs a{dh, lddh, z, ldz, m, n, dz, lddz, q, ldq, scales, qt, ldqt, scales_t, h, ldh, qht, ldqht, scales_ht, row_end};
+  hipStream_t s = (hipStream_t)stream;
+  switch (act) {
+    case FP8BS_ACT_RELU: return launch_gated_bwd<FP8BS_ACT_RELU>(a, s);
+    case FP8BS_ACT_GELU_TANH: return launch_gated_bwd<FP8BS_ACT_GELU_TANH>(a, s);
+    case FP8BS_ACT_SILU: return launch_gated_bwd<FP8BS_ACT_SILU>(a, s);
+    default: return launch_gated_bwd<FP8BS_ACT_NONE>(a, s);
+  }
+}

@@ -16,6 +16,8 @@ struct SkinnyArgs {
   const int32_t* seg;        // ragged expert segments, or null: one product of m rows
   int64_t num_experts;
   Epilogue epi;
+  int gated;                 // qb, sb hold two weights [2n, .]: c = act(z_gate) * z_up, epi.z [m, 2n] (b_layout 0)
+  float* hf;                 // gated: h in FP32 [m, n] as well, or null (c may be null then)
 };
 
 // What the product takes on the best shape of skinny.hip, in us per 56 blocks of

@@ -15,6 +15,13 @@
 //     (buffer_load ... lds) and gathers them with ds_read_b64_tr_b8 (the layout
 //     of the dgrad slabs in gemm.hip).
 // Rows past the end are read as the last row again and not stored.
+//
+// GATED (b_layout 0): a 16-column MFMA tile holds 8 gate columns and the same 8
+// up columns, weight rows n0 .. n0 + 7 and n + n0 .. n + n0 + 7, so a tile makes 8
+// columns of h = act(gate) * up and a short n still spreads over the chip (n = 2048
+// is 256 workgroups of one tile, where 16 + 16 columns would be 128).  The
+// accumulators of a gate column and of its up column meet in LDS, where the waves'
+// sums are joined anyway.
 
 #include "launch.h"
 #include "skinny.h"
@@ -40,6 +47,22 @@ __device__ __forceinline__ void finish4(const SkinnyArgs& p, int64_t row, int64_
     x[3] += bf16_hi(r.y);
   }
   *reinterpret_cast<uint2*>(p.c + row * p.ldc + col) = pack();
+}
+
+// h = act(gate) * up for 4 consecutive columns of one row -> z out, h in bf16 and FP32
+__device__ __forceinline__ void finish_gated4(const SkinnyArgs& p, int64_t row, int64_t col, float4 gate, float4 up) {
+  float x[4] = {gate.x, gate.y, gate.z, gate.w};
+  const float y[4] = {up.x, up.y, up.z, up.w};
+  if (p.epi.z) {
+    uint16_t* const z = p.epi.z + row * p.epi.ldz + col;
+    *reinterpret_cast<uint2*>(z) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    *reinterpret_cast<uint2*>(z + p.n) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+  }
+  act_forward4(p.epi.act, x);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) x[v] *= y[v];
+  if (p.c) *reinterpret_cast<uint2*>(p.c + row * p.ldc + col) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  if (p.hf) *reinterpret_cast<float4*>(p.hf + row * p.n + col) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
 // The workgroup's rows and weight: a tile of a ragged segment, or of the one product.
@@ -75,6 +98,30 @@ __device__ __forceinline__ void join_waves(const SkinnyArgs& p, float4* part, in
   }
 }
 
+// The same for gated tiles: lanes 0, 1 of a row's four hold 8 gate columns, lanes 2, 3 the up columns.
+template <int WAVES, int TILES, int NT>
+__device__ __forceinline__ void join_waves_gated(const SkinnyArgs& p, const float4* part, int64_t m0, int64_t rows,
+                                                 int64_t n0) {
+  for (int i = threadIdx.x; i < TILES * 32; i += 64 * WAVES) {
+    const int t = i >> 5, r = (i & 31) >> 1, half = i & 1;
+    const int q = t * 64 + 4 * r + half;
+    float4 s[2] = {part[q], part[q + 2]};
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 o = part[w * TILES * 64 + q + 2 * h];
+        s[h].x += o.x;
+        s[h].y += o.y;
+        s[h].z += o.z;
+        s[h].w += o.w;
+      }
+    }
+    const int row = 16 * (t / NT) + r;
+    if (row < rows) finish_gated4(p, m0 + row, n0 + 8 * (t % NT) + 4 * half, s[0], s[1]);
+  }
+}
+
 // U blocks' fragments and scales of one wave
 template <int MT, int NT, int U>
 struct SkinnyGroup {
@@ -83,21 +130,26 @@ struct SkinnyGroup {
   float wb[U], wa[U][MT];
 };
 
-template <int MT, int NT, int kU, int WAVES, bool RAGGED>
+template <int MT, int NT, int kU, int WAVES, bool RAGGED, bool GATED = false>
 __global__ __launch_bounds__(64 * WAVES) void skinny_rows_kernel(SkinnyArgs p, uint32_t tiles_n) {
+  constexpr int kCols = GATED ? 8 : 16;        // output columns of an MFMA tile
   __shared__ float4 part[WAVES * MT * NT * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const uint32_t tm = blockIdx.x / tiles_n;
-  const int64_t n0 = (int64_t)(blockIdx.x - tm * tiles_n) * 16 * NT;
+  const int64_t n0 = (int64_t)(blockIdx.x - tm * tiles_n) * kCols * NT;
   const RaggedTile rt = skinny_tile<MT, RAGGED>(p, (int)tm, lane);
   if (RAGGED && rt.e < 0) return;
   const int64_t K = p.k;
   const int nkb = (int)(K / BK);
 
-  const uint8_t* const wrow = p.qb + ((int64_t)rt.e * p.n + n0 + l16) * K + 32 * g;
-  const float* const wsc = p.sb + ((int64_t)rt.e * (p.n / 128) + n0 / 128) * nkb;
+  // gated: the lane reads weight row l16 % 8 of its half and scales the output columns 4g .. 4g + 3 of its row
+  const int64_t wr = GATED ? (int64_t)rt.e * 2 * p.n + (l16 >> 3) * p.n + n0 + (l16 & 7) : (int64_t)rt.e * p.n + n0 + l16;
+  const int64_t wb = GATED ? (int64_t)rt.e * 2 * (p.n / 128) + (g >> 1) * (p.n / 128) + n0 / 128
+                           : (int64_t)rt.e * (p.n / 128) + n0 / 128;
+  const uint8_t* const wrow = p.qb + wr * K + 32 * g;
+  const float* const wsc = p.sb + wb * nkb;
   const uint8_t* arow[MT];
   const float* asc[MT];
 #pragma unroll
@@ -111,7 +163,7 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_rows_kernel(SkinnyArgs p, u
     for (int u = 0; u < f.kBlocks; ++u) {
       const int k1 = kb + u * WAVES;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) f.b[u][i] = load32(wrow + (int64_t)(16 * i) * K + (int64_t)k1 * BK);
+      for (int i = 0; i < NT; ++i) f.b[u][i] = load32(wrow + (int64_t)(kCols * i) * K + (int64_t)k1 * BK);
       f.wb[u] = wsc[k1];
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
@@ -165,7 +217,8 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_rows_kernel(SkinnyArgs p, u
       part[((wave * MT + j) * NT + i) * 64 + 4 * l16 + g] =
           make_float4(acc[j][i][0], acc[j][i][1], acc[j][i][2], acc[j][i][3]);
   __syncthreads();
-  join_waves<WAVES, MT * NT, NT>(p, part, rt.m0, rt.rows, n0);
+  if constexpr (GATED) join_waves_gated<WAVES, MT * NT, NT>(p, part, rt.m0, rt.rows, n0);
+  else join_waves<WAVES, MT * NT, NT>(p, part, rt.m0, rt.rows, n0);
 }
 
 // b_layout 1.  Each LDS slab its own object, so that the compiler sees that a
@@ -281,13 +334,13 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_cols_kernel(SkinnyArgs p, u
   join_waves<WAVES, MT * 8, 8>(p, part, rt.m0, rt.rows, n0);
 }
 
-// b_layout 0 on 16 MT x 16 NT tiles
-template <int MT, int NT, int U, int WAVES, bool RAGGED>
+// b_layout 0 on 16 MT x 16 NT tiles (gated: 8 NT columns of h)
+template <int MT, int NT, int U, int WAVES, bool RAGGED, bool GATED>
 static int launch_rows(const SkinnyArgs& a, hipStream_t s) {
   const int64_t tiles_m = RAGGED ? ragged_tiles(a.m, a.num_experts, 16 * MT) : (a.m + 16 * MT - 1) / (16 * MT);
-  const int64_t tiles_n = a.n / (16 * NT);
+  const int64_t tiles_n = a.n / ((GATED ? 8 : 16) * NT);
   if (tiles_m * tiles_n > kMaxGrid) return FP8BS_ERR_SHAPE;
-  hipLaunchKernelGGL((skinny_rows_kernel<MT, NT, U, WAVES, RAGGED>), dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WAVES),
+  hipLaunchKernelGGL((skinny_rows_kernel<MT, NT, U, WAVES, RAGGED, GATED>), dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * WAVES),
                      0, s, a, (uint32_t)tiles_n);
   return launch_status();
 }
@@ -320,7 +373,7 @@ static int best_shape(const SkinnyArgs& a, int b_layout, int64_t cus, int64_t* c
   for (int i = 0; i < (b_layout == 0 ? 4 : 2); ++i) {
     const int64_t bm = 16 * s[i].mt;
     const int64_t tiles_m = a.seg ? ragged_tiles(a.m, a.num_experts, bm) : (a.m + bm - 1) / bm;
-    const int64_t c = (tiles_m * (a.n / (16 * s[i].nt)) + cus - 1) / cus * s[i].cost;
+    const int64_t c = (tiles_m * (a.n / ((a.gated ? 8 : 16) * s[i].nt)) + cus - 1) / cus * s[i].cost;
     if (i == 0 || c < *cost) best = i, *cost = c;
   }
   return best;
@@ -332,15 +385,20 @@ int64_t skinny_cost(const SkinnyArgs& a, int b_layout, int64_t cus) {
   return cost;
 }
 
+template <bool RAGGED, bool GATED>
+static int launch_row_shape(const SkinnyArgs& a, int shape, hipStream_t s) {
+  switch (shape) {
+    case 0: return launch_rows<1, 1, 4, 8, RAGGED, GATED>(a, s);
+    case 1: return launch_rows<1, 2, 4, 8, RAGGED, GATED>(a, s);
+    case 2: return launch_rows<2, 2, 2, 8, RAGGED, GATED>(a, s);
+    default: return launch_rows<2, 4, 2, 8, RAGGED, GATED>(a, s);
+  }
+}
+
 template <bool RAGGED>
 static int launch_shape(const SkinnyArgs& a, int b_layout, int shape, hipStream_t s) {
   if (b_layout == 1) return shape == 0 ? launch_cols<1, 4, RAGGED>(a, s) : launch_cols<2, 4, RAGGED>(a, s);
-  switch (shape) {
-    case 0: return launch_rows<1, 1, 4, 8, RAGGED>(a, s);
-    case 1: return launch_rows<1, 2, 4, 8, RAGGED>(a, s);
-    case 2: return launch_rows<2, 2, 2, 8, RAGGED>(a, s);
-    default: return launch_rows<2, 4, 2, 8, RAGGED>(a, s);
-  }
+  return a.gated ? launch_row_shape<RAGGED, true>(a, shape, s) : launch_row_shape<RAGGED, false>(a, shape, s);
 }
 
 int launch_skinny(const SkinnyArgs& a, int b_layout, int64_t cus, hipStream_t s) {

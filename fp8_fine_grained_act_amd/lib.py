@@ -19,7 +19,7 @@ FP8BS_OK = 0
 GROUP = 128
 FP8BS_ACT_NONE, FP8BS_ACT_RELU, FP8BS_ACT_GELU_TANH, FP8BS_ACT_SILU = 0, 1, 2, 3
 
-_c_void_p, _i64, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+_c_void_p, _i64, _int, _double = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
 
 _SIGNATURES = {
     "fp8bs_quantize_act_1x128": [_c_void_p, _i64, _i64, _i64, _int, _c_void_p, _i64, _c_void_p, _c_void_p],
@@ -53,7 +53,31 @@ _SIGNATURES = {
                                   _c_void_p, _i64, _c_void_p],
     "fp8bs_grouped_wgrad_ragged": [_c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p,
                                    _int, _c_void_p],
+    "fp8bs_gemm_gated": [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _int, _c_void_p, _i64, _c_void_p,
+                         _i64, _c_void_p, _i64, _c_void_p, _c_void_p, _i64, _c_void_p],
+    "fp8bs_grouped_gemm_gated_ragged": [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64, _i64,
+                                        _int, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _c_void_p,
+                                        _i64, _c_void_p],
+    "fp8bs_gated_backward": [_c_void_p, _i64, _c_void_p, _i64, _i64, _i64, _int, _c_void_p, _i64, _c_void_p, _i64,
+                             _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, _i64, _c_void_p, _i64, _c_void_p,
+                             _c_void_p, _c_void_p],
+    "fp8bs_adamw_step": [_c_void_p, _i64, _double, _double, _double, _double, _i64, _double, _c_void_p, ctypes.c_uint32,
+                         _c_void_p],
 }
+# host-only calls that return a size
+_SIZES = {
+    "fp8bs_moe_max_rows": [_i64, _i64, _i64],
+    "fp8bs_epilogue_backward_workspace": [_i64, _i64],
+    "fp8bs_gemm_gated_workspace": [_i64, _i64, _i64],
+    "fp8bs_grouped_gemm_gated_ragged_workspace": [_i64, _i64, _i64, _i64],
+}
+
+
+class _AdamwTensor(ctypes.Structure):
+    """fp8bs_adamw_tensor"""
+    _fields_ = [("param", _c_void_p), ("master", _c_void_p), ("grad", _c_void_p), ("avg", _c_void_p), ("sq", _c_void_p),
+                ("avg_scales", _c_void_p), ("root_scales", _c_void_p), ("n", _i64), ("weight_decay", ctypes.c_float),
+                ("param_bf16", ctypes.c_int32), ("grad_bf16", ctypes.c_int32)]
 
 
 class Fp8bsError(RuntimeError):
@@ -74,15 +98,15 @@ def _load():
         fn.restype = ctypes.c_int
     lib.fp8bs_status_string.argtypes = [ctypes.c_int]
     lib.fp8bs_status_string.restype = ctypes.c_char_p
-    lib.fp8bs_moe_max_rows.argtypes = [_i64, _i64, _i64]
-    lib.fp8bs_moe_max_rows.restype = ctypes.c_int64
-    lib.fp8bs_epilogue_backward_workspace.argtypes = [_i64, _i64]
-    lib.fp8bs_epilogue_backward_workspace.restype = ctypes.c_int64
+    for name, args in _SIZES.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int64
     return lib
 
 
 raw = _load()
-EXPORTED = tuple(_SIGNATURES) + ("fp8bs_status_string", "fp8bs_moe_max_rows", "fp8bs_epilogue_backward_workspace")
+EXPORTED = tuple(_SIGNATURES) + ("fp8bs_status_string",) + tuple(_SIZES)
 
 
 def status_string(status):
@@ -702,3 +726,228 @@ def fp8bs_grouped_wgrad_ragged(dy, x, seg_offsets, c=None, accumulate=0, stream=
         raise ValueError("c must be [experts, m, n]")
     _call(raw.fp8bs_grouped_wgrad_ragged, dev, stream, pdy, ldy, px, ldx, pseg, num_e, rows, m, n, pc, accumulate)
     return c
+
+
+def _codes(q, scales, rows, cols, dev, names):
+    """(code address, row stride, scale address) of E4M3 tiles [rows, cols] and their f32 [rows, cols/128]."""
+    if not (isinstance(q, _Tensor) and q.dtype is _u8 and q.get_device() == dev and q.shape == (rows, cols)
+            and q.stride(1) == 1):
+        _refuse(q, _u8, dev, names[0], f"[{rows}, {cols}] with unit column stride")
+    ps = _dense(scales, _f32, dev, names[1])
+    if scales.shape != (rows, cols // GROUP):
+        raise ValueError(f"{names[1]} must be [{rows}, {cols // GROUP}]")
+    return q.data_ptr(), (q.stride(0) if rows > 1 else cols), ps
+
+
+def _code_outputs(q, scales, rows, cols, on, dev, stream, names):
+    """(q, scales, their addresses as _codes gives them) of an optional coded output: q False leaves it out, None
+    allocates it, a tensor is written; scales None allocates them."""
+    if q is False:
+        if scales is not None:
+            raise ValueError(f"{names[1]} goes with {names[0]}")
+        return None, None, (None, 0, None)
+    if q is None:
+        q = _empty((rows, cols), _u8, on, stream)
+    if scales is None:
+        scales = _empty((rows, cols // GROUP), _f32, on, stream)
+    return q, scales, _codes(q, scales, rows, cols, dev, names)
+
+
+def _rows_output(t, rows, cols, on, dev, stream, name):
+    """(t, address, row stride) of an optional bf16 output: False leaves it out, None allocates it."""
+    if t is False:
+        return None, None, 0
+    if t is None:
+        t = _empty((rows, cols), _bf16, on, stream)
+    return (t, *_matrix(t, rows, cols, dev, name))
+
+
+def _workspace(workspace, need, on, dev, stream):
+    """(address, bytes, the tensor to keep until the call has been made)"""
+    if workspace is None and need:
+        workspace = _empty(need // 4, _f32, on, stream)
+    if workspace is None:
+        return None, 0, None
+    return _dense(workspace, _f32, dev, "workspace"), 4 * workspace.numel(), workspace
+
+
+def fp8bs_gemm_gated_workspace(m, n, k):
+    """Bytes of workspace that fp8bs_gemm_gated needs for qh on the current device (host only)."""
+    r = raw.fp8bs_gemm_gated_workspace(m, n, k)
+    if r < 0:
+        raise Fp8bsError("fp8bs_gemm_gated_workspace", r)
+    return r
+
+
+def fp8bs_grouped_gemm_gated_ragged_workspace(num_experts, total_rows, n, k):
+    """The same for fp8bs_grouped_gemm_gated_ragged."""
+    r = raw.fp8bs_grouped_gemm_gated_ragged_workspace(num_experts, total_rows, n, k)
+    if r < 0:
+        raise Fp8bsError("fp8bs_grouped_gemm_gated_ragged_workspace", r)
+    return r
+
+
+def fp8bs_gemm_gated(qa, sa, qb, sb, act=FP8BS_ACT_SILU, z=None, h=None, qh=False, sh=None, workspace=None, stream=None):
+    """A gated block's forward pass: (h bf16 [m, n], qh, sh) with h = act(A Wg^T) * (A Wu^T), qb [2n, k] the gate rows
+    and then the up rows.
+
+    h / qh: a tensor to write, None to allocate one, False to leave that result out (its place holds None then); qh
+    uint8 [m, n] and sh f32 [m, n/128] are h's 1x128 tiles, the down projection's input.  z bf16 [m, 2n], filled with
+    the pre-activations when given (for fp8bs_gated_backward).  workspace: a contiguous float32 tensor of at least
+    fp8bs_gemm_gated_workspace(m, n, k) bytes, or None to allocate one."""
+    dev = _device_of(qa, "qa")
+    pqa, psa = _dense(qa, _u8, dev, "qa"), _dense(sa, _f32, dev, "sa")
+    pqb, psb = _dense(qb, _u8, dev, "qb"), _dense(sb, _f32, dev, "sb")
+    if qa.dim() != 2 or qb.dim() != 2:
+        raise ValueError("qa and qb must be matrices")
+    m, k = qa.shape
+    rows = qb.shape[0]
+    if qb.shape[1] != k or rows % 2 or sa.shape != (m, k // GROUP) or sb.shape != (rows // GROUP, k // GROUP):
+        raise ValueError("operand and scale shapes do not match")
+    n, on = rows // 2, qa.device
+    pz, ldz = (None, 0) if z is None else _matrix(z, m, 2 * n, dev, "z")
+    h, ph, ldh = _rows_output(h, m, n, on, dev, stream, "h")
+    qh, sh, (pqh, ldqh, psh) = _code_outputs(qh, sh, m, n, on, dev, stream, ("qh", "sh"))
+    need = 0
+    if pqh is not None and workspace is None:
+        with torch.cuda.device(dev):
+            need = fp8bs_gemm_gated_workspace(m, n, k)
+    pws, ws_bytes, workspace = _workspace(workspace, need, on, dev, stream)
+    _call(raw.fp8bs_gemm_gated, dev, stream, pqa, psa, pqb, psb, m, n, k, act, pz, ldz, ph, ldh, pqh, ldqh, psh, pws,
+          ws_bytes)
+    return h, qh, sh
+
+
+def fp8bs_grouped_gemm_gated_ragged(qa, sa, seg_offsets, qb, sb, act=FP8BS_ACT_SILU, z=None, h=None, qh=False, sh=None,
+                                    workspace=None, stream=None):
+    """fp8bs_gemm_gated over expert segments of any length: qb [E, 2n, k], sb [E, 2n/128, k/128]; seg_offsets int32
+    [E+1] on the device.  Output rows outside every segment are left as they are."""
+    dev = _device_of(qa, "qa")
+    pqa, psa = _dense(qa, _u8, dev, "qa"), _dense(sa, _f32, dev, "sa")
+    pqb, psb = _dense(qb, _u8, dev, "qb"), _dense(sb, _f32, dev, "sb")
+    pseg = _dense(seg_offsets, _i32, dev, "seg_offsets")
+    if qa.dim() != 2 or qb.dim() != 3:
+        raise ValueError("qa must be [rows, k] and qb [experts, 2n, k]")
+    rows, k = qa.shape
+    num_e, b_rows, b_cols = qb.shape
+    if b_cols != k or b_rows % 2 or sa.shape != (rows, k // GROUP) or sb.shape != (num_e, b_rows // GROUP, k // GROUP):
+        raise ValueError("operand and scale shapes do not match")
+    if seg_offsets.numel() != num_e + 1:
+        raise ValueError("seg_offsets must have num_experts + 1 entries")
+    n, on = b_rows // 2, qa.device
+    pz, ldz = (None, 0) if z is None else _matrix(z, rows, 2 * n, dev, "z")
+    h, ph, ldh = _rows_output(h, rows, n, on, dev, stream, "h")
+    qh, sh, (pqh, ldqh, psh) = _code_outputs(qh, sh, rows, n, on, dev, stream, ("qh", "sh"))
+    need = 0
+    if pqh is not None and workspace is None:
+        with torch.cuda.device(dev):
+            need = fp8bs_grouped_gemm_gated_ragged_workspace(num_e, rows, n, k)
+    pws, ws_bytes, workspace = _workspace(workspace, need, on, dev, stream)
+    _call(raw.fp8bs_grouped_gemm_gated_ragged, dev, stream, pqa, psa, pseg, num_e, rows, pqb, psb, n, k, act, pz, ldz, ph,
+          ldh, pqh, ldqh, psh, pws, ws_bytes)
+    return h, qh, sh
+
+
+def fp8bs_gated_backward(dh, z, act=FP8BS_ACT_SILU, dz=None, q=False, scales=None, qt=False, scales_t=None, h=False,
+                         qht=False, scales_ht=None, row_end=None, stream=None):
+    """A gated block's backward pass from dh bf16 [m, n] and the kept z = [g, u] bf16 [m, 2n]:
+    dz = [dh u act'(g), dh act(g)] and h = act(g) u.  Returns (dz, q, scales, qt, scales_t, h, qht, scales_ht).
+
+    dz, h bf16; q uint8 [m, 2n] and scales f32 [m, 2n/128]: dz's tiles along the columns; qt uint8 [2n, m] and scales_t
+    [2n, m/128]: along the rows, transposed; qht [n, m] and scales_ht: the same of h.  Each of dz, q, qt, h, qht: a
+    tensor to write, None to allocate one, False to leave it out (None in its place).  row_end: int32 [1] on the device,
+    rows from there on are left alone (seg_offsets[-1:])."""
+    dev = _device_of(dh, "dh")
+    if dh.dim() != 2:
+        raise ValueError("dh must be a bf16 matrix")
+    m, n = dh.shape
+    on = dh.device
+    pdh, lddh = _matrix(dh, m, n, dev, "dh")
+    pz, ldz = _matrix(z, m, 2 * n, dev, "z")
+    dz, pdz, lddz = _rows_output(dz, m, 2 * n, on, dev, stream, "dz")
+    h, ph, ldh = _rows_output(h, m, n, on, dev, stream, "h")
+    q, scales, (pq, ldq, ps) = _code_outputs(q, scales, m, 2 * n, on, dev, stream, ("q", "scales"))
+    qt, scales_t, (pqt, ldqt, pst) = _code_outputs(qt, scales_t, 2 * n, m, on, dev, stream, ("qt", "scales_t"))
+    qht, scales_ht, (pqht, ldqht, psht) = _code_outputs(qht, scales_ht, n, m, on, dev, stream, ("qht", "scales_ht"))
+    pend = None
+    if row_end is not None:
+        pend = _dense(row_end, _i32, dev, "row_end")
+        if row_end.numel() != 1:
+            raise ValueError("row_end must hold one number")
+    _call(raw.fp8bs_gated_backward, dev, stream, pdh, lddh, pz, ldz, m, n, act, pdz, lddz, pq, ldq, ps, pqt, ldqt, pst, ph,
+          ldh, pqht, ldqht, psht, pend)
+    return dz, q, scales, qt, scales_t, h, qht, scales_ht
+
+
+class AdamwTable:
+    """Tensors of an optimizer step as fp8bs_adamw_step takes them.  Holds the tensors' memory: a parameter or gradient
+    that is given other memory later (``p.data = ...``, ``p.grad = None``) needs a new table."""
+
+    __slots__ = ("entries", "count", "device", "_kept")
+
+    def __init__(self, entries, count, device, kept):
+        self.entries, self.count, self.device, self._kept = entries, count, device, kept
+
+
+def fp8bs_adamw_table(params, grads, avg, sq, master=None, avg_scales=None, root_scales=None, weight_decay=0.0):
+    """The table of an optimizer step, made once: lists of equal length of contiguous tensors on one device.
+
+    params bf16 or f32; grads f32 or bf16; avg, sq: m and v in f32, or (uint8, with avg_scales and root_scales, f32
+    [ceil(n / 128)] each) the codes of m and of sqrt(v); master: f32 copies of bf16 params (a list, entries may be None,
+    or None); avg_scales, root_scales: lists (entries None where the states are f32) or None; weight_decay: a number or
+    a list of numbers."""
+    params, grads, avg, sq = list(params), list(grads), list(avg), list(sq)
+    count = len(params)
+    spread = lambda x: [None] * count if x is None else list(x)  # noqa: E731
+    master, avg_scales, root_scales = spread(master), spread(avg_scales), spread(root_scales)
+    decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
+    if not all(len(x) == count for x in (grads, avg, sq, master, avg_scales, root_scales, decay)):
+        raise ValueError("the lists must have the same length")
+    entries, kept, dev = (_AdamwTensor * count)(), [], None
+    for i in range(count):
+        p, g = params[i], grads[i]
+        if dev is None:
+            dev = _device_of(p, "params[0]")
+        if isinstance(p, _Tensor) and p.dtype not in (_bf16, _f32):
+            raise TypeError(f"params[{i}] must be bfloat16 or float32")
+        if isinstance(g, _Tensor) and g.dtype not in (_bf16, _f32):
+            raise TypeError(f"grads[{i}] must be float32 or bfloat16")
+        eight = avg_scales[i] is not None
+        if eight != (root_scales[i] is not None):
+            raise ValueError("avg_scales and root_scales go together")
+        if master[i] is not None and p.dtype is not _bf16:
+            raise ValueError(f"master[{i}] goes with a bfloat16 parameter")
+        state = _u8 if eight else _f32
+        pp, pg = _dense(p, getattr(p, "dtype", _f32), dev, f"params[{i}]"), _dense(g, getattr(g, "dtype", _f32), dev, f"grads[{i}]")
+        pm, pv = _dense(avg[i], state, dev, f"avg[{i}]"), _dense(sq[i], state, dev, f"sq[{i}]")
+        pw = None if master[i] is None else _dense(master[i], _f32, dev, f"master[{i}]")
+        pms = None if not eight else _dense(avg_scales[i], _f32, dev, f"avg_scales[{i}]")
+        prs = None if not eight else _dense(root_scales[i], _f32, dev, f"root_scales[{i}]")
+        n = p.numel()
+        if any(t is not None and t.numel() != n for t in (g, avg[i], sq[i], master[i])):
+            raise ValueError(f"tensors {i} differ in size")
+        if eight and any(t.numel() != -(-n // GROUP) for t in (avg_scales[i], root_scales[i])):
+            raise ValueError(f"avg_scales[{i}] and root_scales[{i}] must have a number for each 128 elements")
+        entries[i] = _AdamwTensor(pp, pw, pg, pm, pv, pms, prs, n, decay[i], p.dtype is _bf16, g.dtype is _bf16)
+        kept += [t.detach() for t in (p, g, avg[i], sq[i], master[i], avg_scales[i], root_scales[i]) if t is not None]
+    return AdamwTable(entries, count, dev, kept)
+
+
+def fp8bs_adamw_step(table, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, grad_scale=1.0, scalars=None, seed=0, stream=None):
+    """One AdamW step over the tensors of a table (fp8bs_adamw_table), in place.
+
+    scalars: f32 [3] on the device, (lr, grad_scale, step) in place of these arguments, read when the step runs (for a
+    step captured into a graph); seed: the random bits of states in 8 bits, 0 <= seed < 2^32."""
+    if not isinstance(table, AdamwTable):
+        raise TypeError("table must come from fp8bs_adamw_table")
+    if not 0 <= seed < 1 << 32:
+        raise ValueError("seed must be from 0 to 2^32 - 1")
+    if not table.count:
+        return
+    psc = None
+    if scalars is not None:
+        psc = _dense(scalars, _f32, table.device, "scalars")
+        if scalars.numel() != 3:
+            raise ValueError("scalars must hold lr, grad_scale and step")
+    _call(raw.fp8bs_adamw_step, table.device, stream, table.entries, table.count, lr, beta1, beta2, eps, step, grad_scale,
+          psc, seed)

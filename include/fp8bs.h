@@ -541,6 +541,114 @@ int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const uint16_t* 
                                const int32_t* seg_offsets, int64_t num_experts, int64_t total_rows, int64_t m,
                                int64_t n, float* c, int accumulate, void* stream);
 
+/*
+ * ---- A gated feed-forward block ----------------------------------------------
+ * h = act(x Wg^T) * (x Wu^T): the experts and the dense feed-forward layers hold a
+ * gate and an up projection, stacked here as one weight [2n, k], gate rows first
+ * (the experts' gate and up weights are among the FP8 GEMMs, deepseek.csdn.net page,
+ * section 一(二); what surrounds the products stays in FP32 and bf16, section 二(四)).
+ */
+
+/*
+ * Forward: g = A Wg^T, u = A Wu^T (each as fp8bs_gemm, b_layout 0), h = act(g) * u in FP32.
+ *   qa  E4M3 [m, k] contiguous, sa f32 [m, k/128] contiguous
+ *   qb  E4M3 [2n, k] contiguous, sb f32 [2n/128, k/128]
+ *   act FP8BS_ACT_* (FP8BS_ACT_NONE: h = g * u)
+ *   z   bf16 [m, 2n], row stride ldz, or NULL: g and u side by side, rounded once, for
+ *       fp8bs_gated_backward (h is made from the unrounded values)
+ *   h   bf16 [m, n], row stride ldh, or NULL: h rounded once
+ *   qh, sh  E4M3 [m, n], row stride ldqh bytes, and f32 [m, n/128], or both NULL: the 1x128
+ *       tiles of the unrounded h along the columns, the down projection's input (s =
+ *       amax / 448, codes of the quotient as fp8bs_quantize_act_1x128 takes it)
+ *   workspace  16-byte aligned, at least fp8bs_gemm_gated_workspace(m, n, k) bytes, used only by
+ *       this call until it has run (two captured graphs that may run at once need one
+ *       each); may be NULL where that is 0 or qh is NULL
+ *   n is the width of h.  m >= 1 (any), n % 128 == 0, k % 128 == 0, 2 n k < 2^32,
+ *   256 k < 2^32 - 1, m (n / 16) < 2^31; h or qh is needed.  The outputs must not overlap each other or an input.
+ * Alignment: qa, qb, z, h, qh 16 bytes, ldz and ldh % 8 == 0, ldqh % 16 == 0, sa, sb, sh
+ * 4 bytes.  Never allocates.  Errors: FP8BS_ERR_SCRATCH when the workspace is missing or too small.
+ */
+int fp8bs_gemm_gated(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t m, int64_t n,
+                     int64_t k, int act, uint16_t* z, int64_t ldz, uint16_t* h, int64_t ldh, uint8_t* qh, int64_t ldqh,
+                     float* sh, float* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace fp8bs_gemm_gated needs for qh on the current device (host only; 0: none); a negative status for sizes it refuses. */
+int64_t fp8bs_gemm_gated_workspace(int64_t m, int64_t n, int64_t k);
+
+/*
+ * The same over expert segments of any length (see above: offsets are clipped, rows that
+ * belong to no segment are neither read nor written): qb E4M3 [num_experts, 2n, k], sb f32
+ * [num_experts, 2n/128, k/128], rows as for fp8bs_grouped_gemm_ragged, outputs with
+ * total_rows rows.  total_rows == 0: nothing is done.
+ */
+int fp8bs_grouped_gemm_gated_ragged(const uint8_t* qa, const float* sa, const int32_t* seg_offsets, int64_t num_experts,
+                                    int64_t total_rows, const uint8_t* qb, const float* sb, int64_t n, int64_t k, int act,
+                                    uint16_t* z, int64_t ldz, uint16_t* h, int64_t ldh, uint8_t* qh, int64_t ldqh, float* sh,
+                                    float* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t total_rows, int64_t n, int64_t k);
+
+/*
+ * Backward, from one read of dh and the kept z = [g, u]:
+ *   dz = [dh u act'(g), dh act(g)],   h = act(g) u        (FP32, act' at the stored bf16 g; relu'(0) = 0)
+ * in any of the forms that the products of the backward pass read; each may be NULL, not all:
+ *   dh  bf16 [m, n], row stride lddh           z  bf16 [m, 2n], row stride ldz
+ *   dz  bf16 [m, 2n], row stride lddz          h  bf16 [m, n], row stride ldh (the experts' weight gradients)
+ *   q, scales      E4M3 [m, 2n], row stride ldq, f32 [m, 2n/128]: tiles of dz along the columns (activation
+ *                  gradient: fp8bs_gemm or fp8bs_grouped_gemm_ragged, b_layout 1, with the stacked weight as stored)
+ *   qt, scales_t   E4M3 [2n, m], row stride ldqt, f32 [2n, m/128]: tiles of dz along the rows, transposed
+ *   qht, scales_ht E4M3 [n, m], row stride ldqht, f32 [n, m/128]: the same of h (weight gradients: fp8bs_gemm_wgrad)
+ *   row_end  int32 on the device, or NULL: rows from *row_end on are neither read nor written (the end of the
+ *            last expert segment, seg_offsets + num_experts)
+ * Codes are those of the unrounded FP32 values.  m >= 1, n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
+ * m % 128 == 0 and row_end NULL, m < 2^23.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an input, but dz may be z (same
+ * pointer and stride) where neither qt nor qht is asked for, and h may be dh.
+ * Alignment: bf16 and code pointers 16 bytes, bf16 strides % 8 == 0, code strides % 16 == 0, scales and row_end 4 bytes.
+ */
+int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int64_t ldz, int64_t m, int64_t n, int act,
+                         uint16_t* dz, int64_t lddz, uint8_t* q, int64_t ldq, float* scales, uint8_t* qt, int64_t ldqt,
+                         float* scales_t, uint16_t* h, int64_t ldh, uint8_t* qht, int64_t ldqht, float* scales_ht,
+                         const int32_t* row_end, void* stream);
+
+/*
+ * ---- The optimizer step ---------------------------------------------------------
+ * AdamW over many tensors at once, from the FP32 (or bf16) gradients of the weight-gradient
+ * products, with its states in FP32 or in 8 bits (deepseek.csdn.net page, section 二(四):
+ * low-precision storage of the optimizer states, FP32 master weights):
+ *   g = grad_scale * grad,   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr (m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay p)
+ */
+typedef struct fp8bs_adamw_tensor {
+  void* param;          /* bf16 or f32 [n]; written                                                        */
+  float* master;        /* f32 [n], or NULL.  With it (bf16 params only) p is read and kept here, and param gets p rounded */
+  const void* grad;     /* f32 or bf16 [n]                                                                 */
+  void* avg;            /* m: f32 [n], or E4M3 codes [n]                                                   */
+  void* sq;             /* v: f32 [n], or E4M3 codes of sqrt(v) [n]                                        */
+  float* avg_scales;    /* NULL for f32 states; f32 [ceil(n / 128)]: m = scale * code                      */
+  float* root_scales;   /* with avg_scales: sqrt(v) = scale * code                                         */
+  int64_t n;            /* 0 <= n < 2^32; 0: skipped                                                       */
+  float weight_decay;
+  int32_t param_bf16;   /* 1: param is bf16, 0: f32 */
+  int32_t grad_bf16;    /* 1: grad is bf16, 0: f32  */
+} fp8bs_adamw_tensor;
+
+/*
+ * One step over tensors[0 .. num_tensors) (HOST memory, read before the call returns; types may differ from tensor to
+ * tensor).  All arithmetic in FP32.  States in 8 bits: a scale per 128 consecutive elements (the last group may be
+ * shorter), amax / 448; m rounds to nearest, sqrt(v) to one of its two neighbouring codes at random, upwards with the
+ * probability that its distance from the lower one gives, and never from a positive value to zero.  The update of p
+ * uses the new m and v before they are rounded.  The random bits are a function of (seed, step, the tensor's index in
+ * the table, the element's index), so equal calls give equal bits.
+ *   scalars  f32 [3] on the device: lr, grad_scale and step (a whole number from 1 to 2^24), read when the kernels run
+ *            and in place of the arguments of these names (a step captured into a graph); or NULL
+ * No tensor may overlap another.  0 <= beta < 1, eps >= 0, step >= 1 (else FP8BS_ERR_FLAG).  Never allocates.
+ * Alignment: param, master, grad, avg, sq 16 bytes, scales and scalars 4 bytes.  FP8BS_ERR_NULL also when exactly one
+ * of avg_scales, root_scales is NULL; FP8BS_ERR_FLAG for a master beside an f32 param.  Everything is checked before
+ * the first kernel is enqueued.
+ */
+int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_tensors, double lr, double beta1, double beta2,
+                     double eps, int64_t step, double grad_scale, const float* scalars, uint32_t seed, void* stream);
+
 /* Short English text for a status code (static storage, never NULL). */
 const char* fp8bs_status_string(int status);
 
