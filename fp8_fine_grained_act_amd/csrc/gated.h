@@ -12,4 +12,9 @@ struct GatedArgs {
   float* sh;                 // their scales [m, n/128]
 };
 
+// The kernel of a gated product (gemm.hip): 0 for the few-row tiles of skinny.hip, else the
+// weight rows of a warp-specialized tile, 128 (64 columns of h) or 256 (128 columns, whose rows' codes it makes itself).
+int gated_tile_cols(const GatedArgs& a, int64_t cus);
+int launch_gated_tiles(const GatedArgs& a, int bn, hipStream_t s);
+
 }  // namespace fp8bs

@@ -292,35 +292,46 @@ static int gated_check(const GatedArgs& a, float* workspace) {
   return FP8BS_OK;
 }
 
-static int64_t gated_workspace(const GatedArgs& a) { return a.qh ? 4 * a.p.m * a.p.n : 0; }
+// h in FP32, for the kernels whose tiles do not hold a row's 128 columns
+static int64_t gated_workspace(const GatedArgs& a, int bn) { return a.qh && bn != 256 ? 4 * a.p.m * a.p.n : 0; }
 
 static int gated_run(GatedArgs a, float* workspace, int64_t workspace_bytes, hipStream_t s) {
-  const int64_t need = gated_workspace(a);
+  const int64_t cus = cu_count();
+  const int bn = gated_tile_cols(a, cus);
+  const int64_t need = gated_workspace(a, bn);
   if (need > 0 && (!workspace || workspace_bytes < need)) return FP8BS_ERR_SCRATCH;
   a.p.hf = need > 0 ? workspace : nullptr;
-  int st = launch_skinny(a.p, 0, cu_count(), s);
-  if (st == FP8BS_OK && a.qh) st = quant_h(a, s);
+  int st = bn ? launch_gated_tiles(a, bn, s) : launch_skinny(a.p, 0, cus, s);
+  if (st == FP8BS_OK && need > 0) st = quant_h(a, s);
   return st;
 }
 
-extern "C" int64_t fp8bs_gemm_gated_workspace(int64_t m, int64_t n, int64_t k) {
+// The workspace of sizes alone: seg for expert segments (its contents do not count).
+static int64_t gated_workspace_of(int64_t m, int64_t n, int64_t k, int64_t num_experts, const int32_t* seg) {
   GatedArgs a{};
   if (m <= 0 || k <= 0) return FP8BS_ERR_SHAPE;
   a.p.m = m;
   a.p.n = n;
   a.p.k = k;
   a.p.gated = 1;
-  a.p.num_experts = 1;
-  a.qh = reinterpret_cast<uint8_t*>(16);
+  a.p.num_experts = num_experts;
+  a.p.seg = seg;
+  a.qh = reinterpret_cast<uint8_t*>(16);       // any aligned address: not used
   a.sh = reinterpret_cast<float*>(16);
-  a.ldqh = n > 0 ? (n + 15) / 16 * 16 : 0;
+  a.ldqh = n > 0 ? n : 0;
   const int st = gated_check(a, nullptr);
-  return st == FP8BS_OK ? gated_workspace(a) : st;
+  return st == FP8BS_OK ? gated_workspace(a, gated_tile_cols(a, cu_count())) : st;
+}
+
+extern "C" int64_t fp8bs_gemm_gated_workspace(int64_t m, int64_t n, int64_t k) {
+  return gated_workspace_of(m, n, k, 1, nullptr);
 }
 
 extern "C" int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t total_rows, int64_t n, int64_t k) {
-  if (num_experts < 1 || num_experts > 65536 || total_rows < 0 || total_rows > 0x3FFFFFFFLL) return FP8BS_ERR_SHAPE;
-  return total_rows == 0 ? 0 : fp8bs_gemm_gated_workspace(total_rows, n, k);
+  if (num_experts < 1 || num_experts > 65536 || total_rows < 0 || total_rows > 0x3FFFFFFFLL || k <= 0 || n <= 0 || n % 128 ||
+      k % BK)
+    return FP8BS_ERR_SHAPE;
+  return total_rows == 0 ? 0 : gated_workspace_of(total_rows, n, k, num_experts, reinterpret_cast<const int32_t*>(16));
 }
 
 extern "C" int fp8bs_gemm_gated(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb, int64_t m, int64_t n,

@@ -49,8 +49,8 @@
 #include <type_traits>
 
 #include "common.h"
+#include "gated.h"
 #include "launch.h"
-#include "skinny.h"
 
 namespace fp8bs {
 
@@ -58,8 +58,9 @@ enum GemmMode : int { kFprop = 0, kDgrad = 1, kWgrad = 2, kGrouped = 3 };
 
 // What a forward or dgrad kernel does beside the plain product: kEpi applies
 // bias, activation and residual before the bf16 rounding (store_row_epi),
-// kRagged walks expert segments of any length (ragged_tile).
-enum GemmVariant : int { kPlain = 0, kEpi = 1, kRagged = 2 };
+// kRagged walks expert segments of any length (ragged_tile), kGated multiplies
+// by a gate and an up weight at once (store_rows_gated), kGatedRagged does both.
+enum GemmVariant : int { kPlain = 0, kEpi = 1, kRagged = 2, kGated = 3, kGatedRagged = 4 };
 
 struct GemmArgs {
   const uint8_t* qa;
@@ -85,7 +86,11 @@ struct GemmArgs {
   int tile_sel;              // grouped: 0 every tile, 1 only each expert's first m-tile, 2 the others
   int keep_all;              // grouped from bf16 weights with qw: 1 every expert's codes stored, 0 only
                              // those of experts with several m-tiles (the ones read back)
-  Epilogue epi;              // kEpi
+  Epilogue epi;              // kEpi; gated: z [m, 2n] and act (n is the width of h, c = h in bf16 or null)
+  float* hf;                 // gated: h in FP32 [m, n], or null
+  uint8_t* qh;               // gated: codes and scales of h's 1x128 tiles, or null (128 x 256 tiles only)
+  int64_t ldqh;
+  float* sh;
 };
 
 // Expert whose segment holds row m0: the largest e with seg[e] <= m0 (empty
@@ -352,6 +357,43 @@ __device__ __forceinline__ void store_row_epi(const GemmArgs& p, const v4f (&acc
       y[3] += bf16_hi(r1[1]);
     }
     store_pair(crow + col, x, y, p.stream_out);
+  }
+}
+
+// One 16-row group of a gated tile: tiles 0, 1 hold the gate's 32 columns, tiles 2, 3
+// the up projection's.  z goes out as it is, then h = act(gate) * up, which stays in
+// the gate's accumulators for its codes (rows that are not `live` too: zeros).
+template <int TN, int TM>
+__device__ __forceinline__ void store_row_gated(const GemmArgs& p, v4f (&acc)[TN][TM], int j, int64_t row, int64_t col0,
+                                                int g, bool live) {
+  static_assert(TN == 4, "two tiles of gate columns, two of up columns");
+  float x[2][4], y[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      x[i][v] = acc[i][j][v];
+      y[i][v] = acc[i + 2][j][v];
+    }
+  }
+  const int64_t col = col0 + 16 * (g & 1) + 8 * (g >> 1);
+  if (p.epi.z && live) {
+    uint16_t* const z = p.epi.z + row * p.epi.ldz + col;
+    store_pair(z, x[0], x[1], p.stream_out);
+    store_pair(z + p.n, y[0], y[1], p.stream_out);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    act_forward4(p.epi.act, x[i]);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[i][j][v] = x[i][v] *= y[i][v];
+  }
+  if (!live) return;
+  if (p.c) store_pair(reinterpret_cast<uint16_t*>(p.c) + row * p.ldc + col, x[0], x[1], p.stream_out);
+  if (p.hf) {
+    float* const f = p.hf + row * p.n + col0 + 4 * g;
+    *reinterpret_cast<float4*>(f) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+    *reinterpret_cast<float4*>(f + 16) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
   }
 }
 
@@ -912,8 +954,13 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   static_assert((BN == 128 && (BM == 256 || BM == 192 || (VAR != kPlain && BM == 128))) ||
                     ((BN == 256 || BN == 192) && BM == 128 && MODE != kDgrad),
                 "tile shape");
-  static_assert(VAR == kPlain || ((MODE == kFprop || MODE == kDgrad) && !SPLIT && !(VAR == kRagged && PERSIST)),
+  constexpr bool kRag = VAR == kRagged || VAR == kGatedRagged, kGate = VAR == kGated || VAR == kGatedRagged;
+  static_assert(VAR == kPlain || ((MODE == kFprop || MODE == kDgrad) && !SPLIT && !(kRag && PERSIST)),
                 "variants of the bf16-output products");
+  static_assert(!kGate || (MODE == kFprop && BM == 128 && !PERSIST && MW == 8), "gated: forward, one tile per workgroup");
+  // gated: a wave's 64 weight rows are 32 gate rows and the same 32 up rows, so its
+  // patch makes 32 columns of h and a tile BN / 2
+  constexpr int kTileCols = kGate ? BN / 2 : BN;
   // The plain dgrad on 192-row tiles writes its row indexes and copy counts out as
   // a tile's rows and a constant, not from ra0 and jobs(): the same values, which
   // the compiler schedules better there (1500 x 4096 x 4096 28.4 -> 28.0 us, 3000 x
@@ -931,7 +978,9 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // One slab's scales lie nkb * 4 bytes apart, a request to the L2 for every
   // row, which took a third of the copies' requests; four neighbours of a row
   // share one (256 experts of 4096 x 7168 with 128 rows each: 1.94 -> 1.7 ms).
-  __shared__ float sa4[2][VAR == kRagged ? 4 * BM : 1];
+  __shared__ float sa4[2][kRag ? 4 * BM : 1];
+  // gated tiles of 128 columns of h: each row's maximum in the four waves across them
+  __shared__ float tops[kGate && BN == 256 ? WAVES_N : 1][kGate && BN == 256 ? BM : 1];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -948,12 +997,12 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // ragged (one tile per workgroup, row-major): the segment's tile is found
   // once, here, and M is the end of its rows
   RaggedTile rt{0, 0, 0};
-  if constexpr (VAR == kRagged) {
+  if constexpr (kRag) {
     const uint32_t tm = blockIdx.x / (uint32_t)p.tiles_n;
     rt = ragged_tile(p.seg, (int)p.num_experts, p.m, (int)tm, BM, lane);
     if (rt.e < 0) return;                      // more tiles in the grid than the segments hold
   }
-  const int64_t M = VAR == kRagged ? rt.m0 + rt.rows : p.m, N = p.n, K = p.k;
+  const int64_t M = kRag ? rt.m0 + rt.rows : p.m, N = p.n, K = p.k;
   const int nkb = (int)(K / BK);               // K blocks of a row (the width of the scale rows)
   // SPLIT: workgroup (x, y) runs slabs [y * nslab, (y + 1) * nslab) of tile x
   // and stores its FP32 partial to ws[y]; a second kernel sums the partials
@@ -973,9 +1022,9 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   TileMN grouped_tile{0, 0};
   if constexpr (MODE == kGrouped) grouped_tile = tile_coords<W16 ? -3 : 0>(p, blockIdx.x);
   auto tile_origin = [&](int i) {
-    if constexpr (VAR == kRagged) return Origin{rt.m0, (int64_t)(blockIdx.x % (uint32_t)p.tiles_n) * BN};
+    if constexpr (kRag) return Origin{rt.m0, (int64_t)(blockIdx.x % (uint32_t)p.tiles_n) * kTileCols};
     const TileMN t = MODE == kGrouped ? grouped_tile : tile_coords(p, (uint32_t)((int64_t)blockIdx.x + (int64_t)i * G));
-    return Origin{(int64_t)t.m * BM, (int64_t)t.n * BN};
+    return Origin{(int64_t)t.m * BM, (int64_t)t.n * kTileCols};
   };
 
   // grouped: a tile at or past the end of the last segment holds no expert's
@@ -1012,9 +1061,9 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       const int64_t rows_b = N - n0 < BN ? N - n0 : BN;
       const uint8_t* qb = p.qb;
       const float* sb = p.sb;
-      if (VAR == kRagged) {
-        qb += (int64_t)rt.e * N * K;
-        sb += (int64_t)rt.e * (N / 128) * nkb;
+      if (kRag) {
+        qb += (int64_t)rt.e * (kGate ? 2 * N : N) * K;
+        sb += (int64_t)rt.e * (kGate ? 2 * (N / 128) : N / 128) * nkb;
       }
       if (MODE == kGrouped) {
         // expert whose segment holds row m0: the largest e with seg[e] <= m0
@@ -1035,12 +1084,17 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       } else if (MODE == kWgrad) {
         rb = make_rsrc(qb + n0 * K, rows_b * K);
         rsb = make_rsrc(sb + n0 * nkb, rows_b * nkb * 4);
+      } else if (kGate) {                      // from the tile's first gate row to its last up row
+        rb = make_rsrc(qb + n0 * K, (N + kTileCols) * K);
+        rsb = make_rsrc(sb, 2 * (N / 128) * nkb * 4);
       } else {
         rb = make_rsrc(qb + n0 * K, rows_b * K);
         rsb = make_rsrc(sb, (N / 128) * nkb * 4);
       }
       if (MODE == kWgrad) {
         voff_sb = (uint32_t)(scol * nkb) * 4u;
+      } else if (kGate) {                      // 64 weight rows of patch c: 32 gate, 32 up
+        voff_sb = (uint32_t)(((n0 + 32 * c + (lane & 31)) / 128 + (lane >> 5) * (N / 128)) * nkb) * 4u;
       } else {
         const int64_t nb = min((n0 + scol) / 128, N / 128 - 1);   // clipped past the edge
         voff_sb = (uint32_t)(MODE == kDgrad ? nb : nb * nkb) * 4u;
@@ -1068,7 +1122,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     const int my_jobs = A_CP + B_CP + (c < SA_JOBS ? 1 : 0) + (c < SB_JOBS ? 1 : 0);
     auto jobs = [&](int kb) {
       if (kByRow) return my_jobs;
-      return A_CP + B_CP + (VAR == kRagged ? (kb % 4 == 0 ? BM / 64 : 0) : (c < SA_JOBS ? 1 : 0)) + (c < SB_JOBS ? 1 : 0);
+      return A_CP + B_CP + (kRag ? (kb % 4 == 0 ? BM / 64 : 0) : (c < SA_JOBS ? 1 : 0)) + (c < SB_JOBS ? 1 : 0);
     };
     auto issue = [&](int kb, Stage<BM, BN>& s) {
       const uint32_t ks = (uint32_t)kb * BK;
@@ -1079,10 +1133,12 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       for (int i = 0; i < B_CP; ++i) {                              // B copies j = c + 4i (dgrad: 4c + i)
         if (MODE == kDgrad)
           dma16(rb, s.b + (4 * c + i) * 1024, voff_b, (ks + (uint32_t)(8 * i)) * (uint32_t)N);
+        else if (kGate)                        // 32 rows a step: the gate's and the up weight's in turn
+          dma16(rb, s.b + (c + 4 * i) * 1024, voff_b, ks + (uint32_t)(32 * (i >> 1) + (i & 1) * (int)N) * (uint32_t)K);
         else
           dma16(rb, s.b + (c + 4 * i) * 1024, voff_b, ks + (uint32_t)(32 * i) * (uint32_t)K);
       }
-      if (VAR == kRagged) {
+      if (kRag) {
         if (kb % 4 == 0) {
 #pragma unroll
           for (int i = 0; i < BM / 64; ++i)
@@ -1126,7 +1182,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     // per unit (in its last group), else one per unit (at its start); the
     // copy waves pass the prologue barrier plus one per phase, except the
     // last phase in the second case
-    constexpr bool kEarly = MODE != kDgrad && VAR != kRagged;
+    constexpr bool kEarly = MODE != kDgrad && !kRag;
     auto phase = [&](int u, Stage<BM, BN>& fill) {
       if (u + 2 < units) {
         issue_next(fill);
@@ -1141,6 +1197,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       if (u + 1 < units) phase(u + 1, st0);
       if (u + 2 < units) phase(u + 2, st1);
     }
+    if (kGate && BN == 256 && p.qh) barrier(); // the MFMA waves' exchange of h's maxima
     return;
   }
 
@@ -1149,8 +1206,8 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // A wave's 16-row groups: consecutive, or, for ragged segments, dealt to the
   // waves in turn, so that a tile with fewer rows leaves every wave fewer
   // groups (the slab loop then runs only those: see run_groups)
-  constexpr int kGroupRows = VAR == kRagged ? 16 * WAVES_M : 16;
-  const int wrow = VAR == kRagged ? 16 * wm : WM * wm;
+  constexpr int kGroupRows = kRag ? 16 * WAVES_M : 16;
+  const int wrow = kRag ? 16 * wm : WM * wm;
   const int ra0 = wrow + l16, rb0 = WN * wn + l16;
   // rows ra0 + 16t share ra0's swizzle, so tile t adds 16t rows
   const int a_lo = swz(ra0, 2 * g), a_hi = swz(ra0, 2 * g + 1);
@@ -1198,13 +1255,14 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     v8i a0, a1;
     float wa0, wa1;
     float wb0;      // forward / dgrad: one weight block covers the patch's columns
+    float wb1;      // gated: and one its up columns
     float wbs[TN];  // or one per 16-column MFMA tile (kWbPerTile)
     v4f wb[TN];     // weight gradient: a scale per column
   };
   // the row scale of this wave's group t in slab kb
-  constexpr int kScaleStep = (VAR == kRagged ? 4 : 1) * kGroupRows;
+  constexpr int kScaleStep = (kRag ? 4 : 1) * kGroupRows;
   auto row_scales = [&](const Stage<BM, BN>& s, int kb) -> const float* {
-    return VAR == kRagged ? &sa4[(kb >> 2) & 1][4 * ra0 + (kb & 3)] : kByRow ? s.sa : &s.sa[ra0];
+    return kRag ? &sa4[(kb >> 2) & 1][4 * ra0 + (kb & 3)] : kByRow ? s.sa : &s.sa[ra0];
   };
   auto row_scale = [&](const float* sap, int t) { return sap[kByRow ? WM * wm + 16 * t + l16 : kScaleStep * t]; };
   // reads in the order of first use: B fragment 0 and A fragment 0 (the
@@ -1222,6 +1280,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       h.wb0 = 0.f;
     } else {
       h.wb0 = kWbPerTile ? 0.f : s.sb[WN * wn];
+      if (kGate) h.wb1 = s.sb[WN * wn + 32];
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
         h.wbs[i] = kWbPerTile ? s.sb[WN * wn + 16 * i] : 0.f;
@@ -1235,7 +1294,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // LDS instructions of one head, spread over the MFMAs of the group that
   // reads it (issued all at once they queue behind each other and hold up
   // that group's MFMAs)
-  constexpr int kHeadReads = (MODE == kDgrad ? 4 * TN : 2 * TN) + 2 * (2 + 1) + (MODE == kWgrad || kWbPerTile ? TN : 1);
+  constexpr int kHeadReads = (MODE == kDgrad ? 4 * TN : 2 * TN) + 2 * (2 + 1) + (MODE == kWgrad || kWbPerTile ? TN : kGate ? 2 : 1);
   constexpr int kHeadPerMfma = (kHeadReads + TN - 1) / TN;
   auto barrier = [&]() {
     asm volatile("" ::: "memory");
@@ -1267,7 +1326,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
   // MFMAs.  dgrad keeps the barrier at the start of each slab: its head is
   // 16 transposing LDS reads, more than one group's MFMAs hide, and it
   // measured 7% slower with the early head.
-  constexpr bool kEarly = MODE != kDgrad && VAR != kRagged;
+  constexpr bool kEarly = MODE != kDgrad && !kRag;
   if (W16) barrier();                          // the copy waves' exchange of slab 0's block maxima
   Head hd;
   if (kEarly) {
@@ -1290,7 +1349,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
     v8i a_cur = hd.a0, a_n1 = hd.a1;
     float wa_cur = hd.wa0, wa_n1 = hd.wa1;
     v8i na0 = a_cur, na1 = a_n1;
-    float nwa0 = 0.f, nwa1 = 0.f, nwb0 = 0.f;
+    float nwa0 = 0.f, nwa1 = 0.f, nwb0 = 0.f, nwb1 = 0.f;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
       const bool last = j + 1 == GR;
@@ -1305,10 +1364,12 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
         na0 = frag_a(sn.a, 0);
         nwa0 = row_scale(row_scales(sn, kb + 1), 0);
         nwb0 = (MODE == kWgrad || kWbPerTile) ? 0.f : sn.sb[WN * wn];
+        if (kGate) nwb1 = sn.sb[WN * wn + 32];
         na1 = frag_a(sn.a, TM > 1 ? 1 : 0);
         nwa1 = row_scale(row_scales(sn, kb + 1), TM > 1 ? 1 : 0);
       }
       const float wj = MODE == kWgrad ? wa_cur : wa_cur * hd.wb0;
+      const float wj1 = kGate ? wa_cur * hd.wb1 : wj;
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
         const int t = j * TN + i;
@@ -1318,7 +1379,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
         if (t > 0) fold((t - 1) % TN, (t - 1) / TN);
         else fold(TN - 1, GR - 1);
         P_prev = P;
-        pw = kWbPerTile ? wa_cur * hd.wbs[i] : wj;
+        pw = kWbPerTile ? wa_cur * hd.wbs[i] : kGate && i >= TN / 2 ? wj1 : wj;
         if (MODE == kWgrad) pwb = hd.wb[i];
         if (kEarly && last) {                 // fragment i's last use: refill it for slab kb + 1
           hd.bf[i] = frag(sn.b, b_lo, b_hi, i);
@@ -1353,6 +1414,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       hd.wa0 = nwa0;
       hd.wa1 = nwa1;
       hd.wb0 = nwb0;
+      if (kGate) hd.wb1 = nwb1;
     }
   };
   // ---- tile end: fold the pending partial, store, start the next tile ------
@@ -1362,6 +1424,11 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
 #pragma unroll
     for (int j = 0; j < decltype(groups)::value; ++j) {
       const int64_t row = kByRow ? m0 + WM * wm + 16 * j + l16 : m0 + ra0 + kGroupRows * j;
+      if constexpr (kGate) {
+        store_row_gated<TN, TM>(p, acc, j, row, n0 + 32 * wn, g, row < M);
+        __builtin_amdgcn_sched_barrier(0);
+        continue;
+      }
       if (row >= M) continue;
       if (SPLIT) {
         float* prow = p.ws + ((int64_t)blockIdx.y * M + row) * N;
@@ -1390,6 +1457,40 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
         }
       }
       __builtin_amdgcn_sched_barrier(0);     // one row of stores at a time: few live temporaries
+    }
+    if constexpr (kGate && BN == 256) {
+      if (!p.qh) return;
+      // a row's maximum over the tile's 128 columns of h: its wave's 32 columns, then the four waves' in LDS
+#pragma unroll
+      for (int j = 0; j < decltype(groups)::value; ++j) {
+        float t = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) t = fmaxf(t, fmaxf(fabsf(acc[0][j][v]), fabsf(acc[1][j][v])));
+        t = max_xor32_f32(max_xor16_f32(t));
+        if (g == 0) tops[wn][ra0 + kGroupRows * j] = t;
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);      // lgkmcnt(0): in LDS
+      barrier();
+#pragma unroll
+      for (int j = 0; j < decltype(groups)::value; ++j) {
+        const int r = ra0 + kGroupRows * j;
+        const int64_t row = m0 + r;
+        const F32Scale sc = f32_scale(fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r])));
+        uint32_t code[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float q[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) q[v] = f32_quotient<true>(acc[i][j][v], sc);
+          code[i] = code4_f32(q[0], q[1], q[2], q[3]);
+        }
+        const auto sw = __builtin_amdgcn_permlane16_swap(code[0], code[1], false, false);
+        if (row < M) {
+          const int64_t col = n0 + 32 * wn + 16 * (g & 1) + 8 * (g >> 1);
+          *reinterpret_cast<uint2*>(p.qh + row * p.ldqh + col) = make_uint2(sw[0], sw[1]);
+          if (wn == 0 && g == 0) p.sh[row * (N / 128) + n0 / 128] = sc.s;
+        }
+      }
     }
   };
   int ti = 0, tkb = 0;
@@ -1425,7 +1526,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       store_tile(groups);
     }
   };
-  if constexpr (VAR == kRagged) {
+  if constexpr (kRag) {
     // only the groups that hold rows (at least one, so that every wave passes
     // every barrier): a tile of 187 rows takes three quarters of a full one
     static_assert(TM >= 2 && TM <= 4, "the cases below");
@@ -1550,6 +1651,61 @@ static int launch_ws_tiles(GemmArgs a, hipStream_t s) {
   hipLaunchKernelGGL((gemm_ws_kernel<MODE, 8, BM, 128, false, false, false, VAR>), dim3((unsigned)grid), dim3(64 * 12), 0,
                      s, a);
   return launch_status();
+}
+
+// Gated products on 128 x BN tiles (BN / 2 columns of h), one per workgroup.
+template <int BN, int VAR>
+static int launch_gated_tiles(GemmArgs a, hipStream_t s) {
+  a.tiles_n = a.n / (BN / 2);
+  a.tiles_m = VAR == kGatedRagged ? ragged_tiles(a.m, a.num_experts, 128) : (a.m + 127) / 128;
+  GemmArgs both = a;                           // the order is chosen for the stacked weight's product
+  both.n = 2 * a.n;
+  a.group_m = VAR == kGatedRagged ? -1 : choose_group_m(both, 128, BN, 2);
+  const int64_t grid = a.tiles_m * a.tiles_n;
+  if (grid > kMaxGrid) return FP8BS_ERR_SHAPE;
+  hipLaunchKernelGGL((gemm_ws_kernel<kFprop, 8, 128, BN, false, false, false, VAR>), dim3((unsigned)grid), dim3(64 * 12), 0, s,
+                     a);
+  return launch_status();
+}
+
+// What a tile of bn weight rows takes for `rows` rows of a gated product, in skinny.h's unit (ragged_tile_rows' measure).
+static double gated_tile_cost(double rows, int bn) {
+  return fmax(11.5, 4.0 + 4.5 * ceil(rows / 64.0)) * (bn / 128) * 56.0 / 32.0;
+}
+
+int gated_tile_cols(const GatedArgs& a, int64_t cus) {
+  const SkinnyArgs& p = a.p;
+  const double skinny = (double)skinny_cost(p, 0, cus);
+  const int64_t owners = p.num_experts < p.m ? p.num_experts : p.m;
+  const double mean = (double)p.m / (double)owners;
+  const double high = p.seg && owners > 1 ? mean + 2.0 * sqrt(mean) : mean;
+  const double full = floor(high / 128.0), rest = high - 128.0 * full;
+  int best = 0;
+  double best_cost = skinny;
+  for (int bn = 128; bn <= 256; bn += 128) {
+    const double one = full > 0 ? gated_tile_cost(128.0, bn) : gated_tile_cost(rest, bn);
+    const double all = full * gated_tile_cost(128.0, bn) + (rest > 0 ? gated_tile_cost(rest, bn) : 0.0);
+    const double strips = (double)owners * (double)(p.n / (bn / 2)), chip = (double)cus;
+    const double tiles = strips * (full + (rest > 0 ? 1.0 : 0.0));
+    const double cost = p.seg ? fmax(one, strips * all / chip) : one * ceil(tiles / chip);
+    if (cost < best_cost) best = bn, best_cost = cost;
+  }
+  return best;
+}
+
+int launch_gated_tiles(const GatedArgs& a, int bn, hipStream_t s) {
+  const SkinnyArgs& p = a.p;
+  GemmArgs g{p.qa, p.sa, p.qb, p.sb, p.c, p.ldc, p.m, p.n, p.k, p.seg, p.num_experts, 0, 0, 0, 0, nullptr, 1,
+             p.m * p.n * ((p.c ? 2 : 0) + (p.epi.z ? 4 : 0)) > kStreamBytes};
+  g.epi = p.epi;
+  g.hf = p.hf;
+  if (bn == 256) {
+    g.qh = a.qh;
+    g.ldqh = a.ldqh;
+    g.sh = a.sh;
+    return p.seg ? launch_gated_tiles<256, kGatedRagged>(g, s) : launch_gated_tiles<256, kGated>(g, s);
+  }
+  return p.seg ? launch_gated_tiles<128, kGatedRagged>(g, s) : launch_gated_tiles<128, kGated>(g, s);
 }
 
 // Tile height for ragged segments: 64 (gemm_kernel, two workgroups per CU), 128,
