@@ -72,6 +72,17 @@ __device__ __forceinline__ float max_xor32_f32(float v) {
   return __uint_as_float(max(s[0], s[1]));
 }
 
+// two such values at once: a's maximum with the lane 16 (32) away in the even groups (the
+// lower half), b's in the odd ones (the upper half)
+__device__ __forceinline__ float max_swap16_f32(float a, float b) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(max(s[0], s[1]));
+}
+__device__ __forceinline__ float max_swap32_f32(float a, float b) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(max(s[0], s[1]));
+}
+
 // lane-wise max of two pairs of 16-bit unsigned values (one v_pk_max_u16)
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -157,22 +168,33 @@ __device__ __forceinline__ void quant_run(const uint32_t* in, uint32_t* out, con
 }
 
 // Groups of FP32 values that never were bf16 (a gated product, a gradient, an
-// optimizer state): s = amax / 448 and codes of x / s as above.  x / s takes the
-// same two operations, fma(x, r, x * rl): r + rl is 1 / s to about 2^-48, so the
-// result is the correctly rounded quotient but where that lies within 2^-47 of a
-// midpoint of two FP32 values.  For amax below 2^-64 both sides are scaled by 2^64
-// (s may be subnormal); such an s carries fewer bits, so the quotient is clipped to
-// 448 there (elsewhere it stays below 448 (1 + 2^-22), which codes as 448).  Where s
-// underflows to zero (amax < 2^-141) the codes are signed zeros.
+// optimizer state): s = amax / 448 and E4M3 codes, to nearest even, of x / s.
+//   s is correctly rounded: with 1 / 448 correctly rounded, one fma gives the
+//   remainder of the first quotient and one more the correction (below 2^-100, where
+//   the remainder could be subnormal, the division itself).
+//   For amax below 2^-64 both sides of x / s are scaled by 2^64 (s may be subnormal);
+//   such an s carries fewer bits, so the quotient is clipped to 448 there (elsewhere it
+//   stays below 448 (1 + 2^-21), which codes as 448).  Where s underflows to zero
+//   (amax < 2^-141) the codes are signed zeros.
+// F32Scale holds 1 / s as r + rl, to about 2^-46: x / s by f32_quotient, two operations
+// that round once more.  f32_quotient_fast takes x * r alone, within two units in the last
+// place: the code then differs from the exact quotient's only where that lies within
+// 2^-22 of a midpoint between two codes, 2^-18 of a code's own rounding.
 struct F32Scale {
   float s, r, rl, up;
 };
+__device__ __forceinline__ float over_448(float amax) {
+  constexpr float kInv = 1.0f / kE4M3Max;
+  const float q = amax * kInv;
+  const float s = __builtin_fmaf(__builtin_fmaf(-kE4M3Max, q, amax), kInv, q);
+  return amax < 0x1p-100f ? amax / kE4M3Max : s;
+}
 __device__ __forceinline__ F32Scale f32_scale(float amax) {
   F32Scale g;
-  g.s = amax / kE4M3Max;
+  g.s = over_448(amax);
   g.up = amax < 0x1p-64f ? kTinyScale : 1.0f;
   const float d = g.s * g.up;
-  g.r = d == 0.0f ? 0.0f : 1.0f / d;
+  g.r = d == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(d);
   g.rl = __builtin_fmaf(-d, g.r, 1.0f) * g.r;
   return g;
 }
@@ -182,6 +204,10 @@ __device__ __forceinline__ float f32_quotient(float x, const F32Scale& g) {
   if (!SLOW) return __builtin_fmaf(x, g.r, x * g.rl);
   const float v = x * g.up;
   return __builtin_amdgcn_fmed3f(__builtin_fmaf(v, g.r, v * g.rl), -kE4M3Max, kE4M3Max);
+}
+template <bool SLOW>
+__device__ __forceinline__ float f32_quotient_fast(float x, float r, float up) {
+  return SLOW ? __builtin_amdgcn_fmed3f(x * up * r, -kE4M3Max, kE4M3Max) : x * r;
 }
 __device__ __forceinline__ uint32_t code4_f32(float a, float b, float c, float d) {
   const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

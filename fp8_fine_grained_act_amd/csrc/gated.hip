@@ -9,6 +9,8 @@
 // rows, transposed (weight gradients of both weights; h's for the down projection).
 // Bound by HBM: 6 bytes read per element of h, 2 to 10 written.
 
+#include <type_traits>
+
 #include "common.h"
 #include "gated.h"
 #include "launch.h"
@@ -100,19 +102,24 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// 8 codes of one row's tile piece, its scale stored by the tile's first lane (16 lanes a tile)
-__device__ __forceinline__ void store_row_codes(const float (&x)[8], uint8_t* q, float* s, int lane16) {
-  const F32Scale g = f32_scale(max16_f32(top8(x)));
+// 8 codes of one row's tile piece of dg and of du, their scales stored by the tiles' first lane (16 lanes a tile)
+template <bool SLOW>
+__device__ __forceinline__ uint2 row_codes(const float (&x)[8], const F32Scale& g) {
   float v[8];
-  if (__ballot(g.up != 1.0f)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f32_quotient<true>(x[i], g);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f32_quotient<false>(x[i], g);
+  for (int i = 0; i < 8; ++i) v[i] = f32_quotient_fast<SLOW>(x[i], g.r, g.up);
+  return make_uint2(code4_f32(v[0], v[1], v[2], v[3]), code4_f32(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store_row_codes(const float (&dg)[8], const float (&du)[8], uint8_t* qg, uint8_t* qu,
+                                                float* sg, float* su, int lane16) {
+  const F32Scale a = f32_scale(max16_f32(top8(dg))), b = f32_scale(max16_f32(top8(du)));
+  const bool slow = __ballot(fmaxf(a.up, b.up) != 1.0f) != 0;
+  *reinterpret_cast<uint2*>(qg) = slow ? row_codes<true>(dg, a) : row_codes<false>(dg, a);
+  *reinterpret_cast<uint2*>(qu) = slow ? row_codes<true>(du, b) : row_codes<false>(du, b);
+  if (lane16 == 0) {
+    *sg = a.s;
+    *su = b.s;
   }
-  *reinterpret_cast<uint2*>(q) = make_uint2(code4_f32(v[0], v[1], v[2], v[3]), code4_f32(v[4], v[5], v[6], v[7]));
-  if (lane16 == 0) *s = g.s;
 }
 
 // Without transposed outputs: 16 lanes per piece of 128 columns of a row.
@@ -141,8 +148,7 @@ __global__ __launch_bounds__(256) void gated_bwd_rows_kernel(GatedBwdArgs p, uin
   if (p.q) {
     uint8_t* const qr = p.q + row * p.ldq + col;
     float* const sr = p.s + row * (int64_t)(2 * pieces_n) + tb;
-    store_row_codes(dg, qr, sr, lane16);
-    store_row_codes(du, qr + p.n, sr + pieces_n, lane16);
+    store_row_codes(dg, du, qr, qr + p.n, sr, sr + pieces_n, lane16);
   }
 }
 
@@ -155,9 +161,10 @@ __global__ __launch_bounds__(256) void gated_bwd_rows_kernel(GatedBwdArgs p, uin
 // rows of the output: dword d of column c is stored at d ^ (4 * ((c / 8) % 8)), which
 // keeps 16-byte chunks whole and puts a wave's 64 writes on 32 banks, two each.
 template <int ACT, bool STREAM>
-__global__ __launch_bounds__(512) void gated_bwd_square_kernel(GatedBwdArgs p) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_square_kernel(GatedBwdArgs p) {
   __shared__ float tops[3][8][128];            // [dg, du, h][wave][column]
-  __shared__ float4 scl[3][128];               // a column's r, rl, up
+  __shared__ float rcps[3][128], ups[3][128];  // a column's r and up
+  __shared__ int tiny;                         // some up is not 1
   __shared__ __attribute__((aligned(16))) uint32_t codes[3][128 * 32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid & 15, rg = tid >> 4;
@@ -186,24 +193,25 @@ __global__ __launch_bounds__(512) void gated_bwd_square_kernel(GatedBwdArgs p) {
     if (p.q) {
       uint8_t* const qr = p.q + row * p.ldq + col;
       float* const sr = p.s + row * (2 * p.n / kGroup) + blockIdx.x;
-      store_row_codes(x[0][i], qr, sr, cg);
-      store_row_codes(x[1][i], qr + p.n, sr + p.n / kGroup, cg);
+      store_row_codes(x[0][i], x[1][i], qr, qr + p.n, sr, sr + p.n / kGroup, cg);
     }
+    __builtin_amdgcn_sched_barrier(0);         // a row at a time: few live temporaries
   }
   // columns' maxima
+  if (tid == 0) tiny = 0;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
     float t[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 8; ++j)
       t[j] = fmaxf(fmaxf(fabsf(x[q][0][j]), fabsf(x[q][1][j])), fmaxf(fabsf(x[q][2][j]), fabsf(x[q][3][j])));
-      t[j] = max_xor16_f32(t[j]);
-      t[j] = max_xor32_f32(t[j]);
-    }
-    if (lane < 16) {
-      *reinterpret_cast<float4*>(&tops[q][wave][8 * cg]) = make_float4(t[0], t[1], t[2], t[3]);
-      *reinterpret_cast<float4*>(&tops[q][wave][8 * cg + 4]) = make_float4(t[4], t[5], t[6], t[7]);
-    }
+    // over the wave's four groups of 16 lanes, two columns to a swap: afterwards group gr holds
+    // columns 4 (gr % 2) + 2 (gr / 2) and the next of its 8
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t[j] = max_swap16_f32(t[j], t[j + 4]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) t[j] = max_swap32_f32(t[j], t[j + 2]);
+    *reinterpret_cast<float2*>(&tops[q][wave][8 * cg + 4 * ((lane >> 4) & 1) + 2 * (lane >> 5)]) = make_float2(t[0], t[1]);
   }
   __syncthreads();
   if (tid < 384) {
@@ -212,33 +220,33 @@ __global__ __launch_bounds__(512) void gated_bwd_square_kernel(GatedBwdArgs p) {
 #pragma unroll
     for (int w = 1; w < 8; ++w) t = fmaxf(t, tops[q][w][c]);
     const F32Scale g = f32_scale(t);
-    scl[q][c] = make_float4(g.r, g.rl, g.up, 0.0f);
+    rcps[q][c] = g.r;
+    ups[q][c] = g.up;
+    if (g.up != 1.0f) tiny = 1;
     if (q >= q0 && q < nq) {
       float* const s = q == 2 ? p.sht : p.st + (q * p.n) * (p.m / kGroup);
       s[(c0 + c) * (p.m / kGroup) + blockIdx.y] = g.s;
     }
   }
   __syncthreads();
+  auto code_columns = [&](auto slow) {
+    constexpr bool SLOW = decltype(slow)::value;
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    if (q < q0 || q >= nq) continue;
-    F32Scale g[8];
-    bool tiny = false;
+    for (int q = 0; q < 3; ++q) {
+      if (q < q0 || q >= nq) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 v = scl[q][8 * cg + j];
-      g[j] = F32Scale{0.0f, v.x, v.y, v.z};
-      tiny = tiny || v.z != 1.0f;
+      for (int j = 0; j < 8; ++j) {
+        const float r = rcps[q][8 * cg + j], up = SLOW ? ups[q][8 * cg + j] : 1.0f;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f32_quotient_fast<SLOW>(x[q][i][j], r, up);
+        codes[q][(8 * cg + j) * 32 + (rg ^ ((cg & 7) << 2))] = code4_f32(v[0], v[1], v[2], v[3]);
+        __builtin_amdgcn_sched_barrier(0);     // a column at a time: few live scales
+      }
     }
-    const bool slow = __ballot(tiny) != 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = slow ? f32_quotient<true>(x[q][i][j], g[j]) : f32_quotient<false>(x[q][i][j], g[j]);
-      codes[q][(8 * cg + j) * 32 + (rg ^ ((cg & 7) << 2))] = code4_f32(v[0], v[1], v[2], v[3]);
-    }
-  }
+  };
+  if (tiny) code_columns(std::true_type{});
+  else code_columns(std::false_type{});
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < 3; ++q) {

@@ -1658,9 +1658,13 @@ template <int BN, int VAR>
 static int launch_gated_tiles(GemmArgs a, hipStream_t s) {
   a.tiles_n = a.n / (BN / 2);
   a.tiles_m = VAR == kGatedRagged ? ragged_tiles(a.m, a.num_experts, 128) : (a.m + 127) / 128;
-  GemmArgs both = a;                           // the order is chosen for the stacked weight's product
+  // the order is chosen for the stacked weight's product, in bands of 8 m-tiles at most: an
+  // XCD runs 32 tiles at a time, and 8 x 4 of them touch the fewest rows of A and of
+  // the weight (16384 x 2048 x 7168 485 us in bands of 16, 450 in bands of 8)
+  GemmArgs both = a;
   both.n = 2 * a.n;
   a.group_m = VAR == kGatedRagged ? -1 : choose_group_m(both, 128, BN, 2);
+  if (a.group_m > 8) a.group_m = 8;
   const int64_t grid = a.tiles_m * a.tiles_n;
   if (grid > kMaxGrid) return FP8BS_ERR_SHAPE;
   hipLaunchKernelGGL((gemm_ws_kernel<kFprop, 8, 128, BN, false, false, false, VAR>), dim3((unsigned)grid), dim3(64 * 12), 0, s,
@@ -1668,26 +1672,35 @@ static int launch_gated_tiles(GemmArgs a, hipStream_t s) {
   return launch_status();
 }
 
-// What a tile of bn weight rows takes for `rows` rows of a gated product, in skinny.h's unit (ragged_tile_rows' measure).
+// Kernel of a gated product, by what the tiles of every row and column cost: rounds of
+// one tile per CU, in skinny.h's unit (us over 56 blocks without a launch's 4).  A round
+// of 128 x 128 tiles costs 21 with up to 64 rows in a tile and 30 above, one of 128 x
+// 256 tiles 36 and 50: the weight's copies bound a low tile, twice as many of them
+// in the wide one, which multiplies more per byte of A.  Few-row tiles are cheaper up to 128 rows
+// of one weight.  Measured on few-row / 128 / 256 tiles, n 2048, k 7168: 64 rows 19.1 / 25.2 / 39.3 us, 128
+// 25.4 / 29.7 / 40.9, 300 71 / 28.6 / 39.8, 1037 - / 57.9 / 42.5, 4096 - / 137 / 109; 1037 rows of n
+// 1408, k 4096 20.5 / 27.1 on 128 / 256; 256 experts with 64 rows in all 336 / 307 / 289, with 32768
+// rows - / 2005 / 1641, 8 experts of n 512, k 1024 with 1000 rows 10.5 / 12.1 on 128 / 256.  The rows'
+// distribution over experts is taken as in ragged_tile_rows.
 static double gated_tile_cost(double rows, int bn) {
-  return fmax(11.5, 4.0 + 4.5 * ceil(rows / 64.0)) * (bn / 128) * 56.0 / 32.0;
+  if (rows <= 64.0) return bn == 128 ? 21.0 : 36.0;
+  return bn == 128 ? 30.0 : 50.0;
 }
 
 int gated_tile_cols(const GatedArgs& a, int64_t cus) {
   const SkinnyArgs& p = a.p;
-  const double skinny = (double)skinny_cost(p, 0, cus);
-  const int64_t owners = p.num_experts < p.m ? p.num_experts : p.m;
+  const int64_t owners = p.seg ? (p.num_experts < p.m ? p.num_experts : p.m) : 1;
   const double mean = (double)p.m / (double)owners;
-  const double high = p.seg && owners > 1 ? mean + 2.0 * sqrt(mean) : mean;
+  const double high = owners > 1 ? mean + 2.0 * sqrt(mean) : mean;
   const double full = floor(high / 128.0), rest = high - 128.0 * full;
+  const double chip = (double)cus;
   int best = 0;
-  double best_cost = skinny;
+  double best_cost = (double)skinny_cost(p, 0, cus);
   for (int bn = 128; bn <= 256; bn += 128) {
-    const double one = full > 0 ? gated_tile_cost(128.0, bn) : gated_tile_cost(rest, bn);
+    const double strips = (double)owners * (double)(p.n / (bn / 2));
+    const double one = gated_tile_cost(full > 0 ? 128.0 : rest, bn);
     const double all = full * gated_tile_cost(128.0, bn) + (rest > 0 ? gated_tile_cost(rest, bn) : 0.0);
-    const double strips = (double)owners * (double)(p.n / (bn / 2)), chip = (double)cus;
-    const double tiles = strips * (full + (rest > 0 ? 1.0 : 0.0));
-    const double cost = p.seg ? fmax(one, strips * all / chip) : one * ceil(tiles / chip);
+    const double cost = p.seg ? fmax(one, strips * all / chip) : one * ceil(strips * (full + (rest > 0 ? 1.0 : 0.0)) / chip);
     if (cost < best_cost) best = bn, best_cost = cost;
   }
   return best;
