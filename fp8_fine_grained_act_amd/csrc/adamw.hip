@@ -29,7 +29,7 @@
 namespace fp8bs {
 
 constexpr int kPerLaunch = 40;                 // tensors per launch: their table stays below 4 KB of arguments
-constexpr int kAdamwUnroll = 4;
+constexpr int kAdamwUnroll = 2;                // quads of a lane in flight
 constexpr int kAdamwBlock = 1024 * kAdamwUnroll;   // elements per workgroup of 256 threads
 
 struct AdamwTensor {
@@ -51,7 +51,7 @@ struct AdamwArgs {
   int count;
   uint32_t number;                             // of the first tensor
   float lr, beta1, beta2, rest1, rest2, eps, grad_scale;   // rest = 1 - beta
-  float unbias1, unbias2;                      // 1 / (1 - beta^step)
+  float unbias1, root2;                        // 1 / (1 - beta1^step), sqrt(1 / (1 - beta2^step))
   float log1, log2;                            // ln beta, for a step that is on the device
   uint32_t seed, step;
   const float* scalars;                        // lr, grad_scale, step on the device, or null
@@ -66,95 +66,143 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// q in [0, 448] -> the E4M3 value below or above it: 20 random bits added below the
-// last kept bit, the rest cut off; below 2^-6, where the spacing is 2^-9, on the
-// fixed-point value.
+// q in [0, 448] -> the E4M3 value below or above it: 20 random bits added below the last
+// kept bit, the rest cut off.  Below 2^-6 the spacing is 2^-9, that of [2^-6, 2^-5), so q is
+// moved there and back.
 __device__ __forceinline__ float round_at_random(float q, uint32_t bits20) {
-  const float up = __uint_as_float((__float_as_uint(q) + bits20) & ~0xFFFFFu);
-  const float low = floorf(q * 512.0f + (float)bits20 * 0x1p-20f) * 0x1p-9f;
-  return fminf(q >= 0x1p-6f ? up : low, kE4M3Max);
+  const float move = q < 0x1p-6f ? 0x1p-6f : 0.0f;
+  return __uint_as_float((__float_as_uint(q + move) + bits20) & ~0xFFFFFu) - move;
+}
+
+// sqrt(v) to nearest: the hardware's (1 ulp) and one correction by its remainder.  A v so
+// small that the remainder would be subnormal is scaled by 2^64 first.
+__device__ __forceinline__ float sqrt_rn(float v) {
+  const bool low = v < 0x1p-64f;
+  const float x = low ? v * 0x1p64f : v;
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float r = __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * __builtin_amdgcn_rcpf(s), s);
+  return (s > 0.0f ? r : 0.0f) * (low ? 0x1p-32f : 1.0f);
 }
 
 __device__ __forceinline__ float max32_f32(float v) { return max_xor16_f32(max16_f32(v)); }
 
-template <bool EIGHT>
-__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
-  // the workgroup's tensor: the last whose first workgroup is not past this one
-  int k = 0;
-  for (int hi = a.count; hi - k > 1;) {
-    const int mid = (k + hi) >> 1;
-    if (a.block0[mid] <= blockIdx.x) k = mid; else hi = mid;
-  }
-  const AdamwTensor& t = a.t[k];
-  float lr = a.lr, gs = a.grad_scale, u1 = a.unbias1, u2 = a.unbias2;
-  uint32_t step = a.step;
-  if (a.scalars) {
-    lr = a.scalars[0];
-    gs = a.scalars[1];
-    const float n = a.scalars[2];
-    step = (uint32_t)n;
-    u1 = -1.0f / expm1f(n * a.log1);
-    u2 = -1.0f / expm1f(n * a.log2);
-  }
-  uint32_t key = 0;
-  if (EIGHT) key = mix32(mix32(a.seed + step * 0x9E3779B1u) + (a.number + (uint32_t)k) * 0x3C6EF373u);
-  const int64_t base = (int64_t)(blockIdx.x - a.block0[k]) * kAdamwBlock + 4 * threadIdx.x;
+struct AdamwStep {
+  float lr, grad_scale, unbias1, root2;        // root2 = sqrt(1 / (1 - beta2^step))
+  uint32_t key;
+};
 
-  float p[kAdamwUnroll][4], g[kAdamwUnroll][4], m[kAdamwUnroll][4], v[kAdamwUnroll][4];
-  float ms[kAdamwUnroll], rs[kAdamwUnroll];
-  uint32_t mc[kAdamwUnroll], rc[kAdamwUnroll];
-  auto load4 = [](float (&x)[4], const float* src, int64_t i, int64_t n) {
-    if (i + 4 <= n) {
-      const float4 w = *reinterpret_cast<const float4*>(src + i);
-      x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+// 4 consecutive elements per lane.  FULL: all inside the tensor; else elements from n on read as
+// zero and are not written.  STREAM: non-temporal accesses.
+template <bool FULL, bool STREAM>
+struct Quad {
+  int64_t n;
+  template <typename T>
+  __device__ __forceinline__ T get(const void* p) const {
+    return STREAM ? __builtin_nontemporal_load(static_cast<const T*>(p)) : *static_cast<const T*>(p);
+  }
+  template <typename T>
+  __device__ __forceinline__ void put(void* p, T v) const {
+    if (STREAM) __builtin_nontemporal_store(v, static_cast<T*>(p));
+    else *static_cast<T*>(p) = v;
+  }
+  typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+  __device__ __forceinline__ void load(float (&x)[4], const float* src, int64_t i) const {
+    if (FULL || i + 4 <= n) {
+      const v4f w = get<v4f>(src + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = w[j];
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = i + j < n ? src[i + j] : 0.0f;
     }
-  };
-  auto load4_bf16 = [](float (&x)[4], const uint16_t* src, int64_t i, int64_t n) {
-    if (i + 4 <= n) {
-      const uint2 w = *reinterpret_cast<const uint2*>(src + i);
+  }
+  __device__ __forceinline__ void load(float (&x)[4], const uint16_t* src, int64_t i) const {
+    if (FULL || i + 4 <= n) {
+      const u32x2 w = get<u32x2>(src + i);
       x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = i + j < n ? __uint_as_float((uint32_t)src[i + j] << 16) : 0.0f;
     }
-  };
-  auto load4_code = [](const uint8_t* src, int64_t i, int64_t n) -> uint32_t {
-    if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(src + i);
+  }
+  __device__ __forceinline__ uint32_t load_codes(const void* codes, int64_t i) const {
+    const uint8_t* const src = static_cast<const uint8_t*>(codes);
+    if (FULL || i + 4 <= n) return get<uint32_t>(src + i);
     uint32_t w = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) w |= i + j < n ? (uint32_t)src[i + j] << (8 * j) : 0u;
     return w;
-  };
-#pragma unroll
-  for (int u = 0; u < kAdamwUnroll; ++u) {
-    const int64_t i = base + 1024 * u;
-    if (t.grad_bf16) load4_bf16(g[u], static_cast<const uint16_t*>(t.grad), i, t.n);
-    else load4(g[u], static_cast<const float*>(t.grad), i, t.n);
-    if (t.master) load4(p[u], t.master, i, t.n);
-    else if (t.param_bf16) load4_bf16(p[u], static_cast<const uint16_t*>(t.param), i, t.n);
-    else load4(p[u], static_cast<const float*>(t.param), i, t.n);
-    if (EIGHT) {
-      mc[u] = load4_code(static_cast<const uint8_t*>(t.avg), i, t.n);
-      rc[u] = load4_code(static_cast<const uint8_t*>(t.sq), i, t.n);
-      ms[u] = i < t.n ? t.avg_scales[i / kGroup] : 0.0f;
-      rs[u] = i < t.n ? t.root_scales[i / kGroup] : 0.0f;
-    } else {
-      load4(m[u], static_cast<const float*>(t.avg), i, t.n);
-      load4(v[u], static_cast<const float*>(t.sq), i, t.n);
-    }
   }
-  auto store4 = [](float* dst, const float (&x)[4], int64_t i, int64_t n) {
-    if (i + 4 <= n) {
-      *reinterpret_cast<float4*>(dst + i) = make_float4(x[0], x[1], x[2], x[3]);
+  __device__ __forceinline__ void store(float* dst, const float (&x)[4], int64_t i) const {
+    if (FULL || i + 4 <= n) {
+      put<v4f>(dst + i, v4f{x[0], x[1], x[2], x[3]});
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (i + j < n) dst[i + j] = x[j];
     }
-  };
+  }
+  __device__ __forceinline__ void store(uint16_t* dst, const float (&x)[4], int64_t i) const {
+    const u32x2 w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+    if (FULL || i + 4 <= n) {
+      put<u32x2>(dst + i, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) dst[i + j] = (uint16_t)((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+    }
+  }
+  __device__ __forceinline__ void store_codes(void* codes, uint32_t w, int64_t i) const {
+    uint8_t* const dst = static_cast<uint8_t*>(codes);
+    if (FULL || i + 4 <= n) {
+      put<uint32_t>(dst + i, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) dst[i + j] = (uint8_t)(w >> (8 * j));
+    }
+  }
+};
+
+// codes of a group's m (to nearest) and r (at random)
+template <bool SLOW>
+__device__ __forceinline__ uint2 state_codes(const float (&m)[4], const float (&r)[4], const F32Scale& mg, const F32Scale& rg,
+                                             uint32_t random) {
+  float mq[4], rq[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    mq[j] = f32_quotient<SLOW>(m[j], mg);
+    const float q = fminf(f32_quotient<SLOW>(r[j], rg), kE4M3Max);
+    rq[j] = fmaxf(round_at_random(q, mix32(random + (uint32_t)j * 0x9E3779B1u) >> 12), r[j] > 0.0f ? 0x1p-9f : 0.0f);
+  }
+  return make_uint2(code4_f32(mq[0], mq[1], mq[2], mq[3]), code4_f32(rq[0], rq[1], rq[2], rq[3]));
+}
+
+template <bool EIGHT, bool FULL, bool STREAM>
+__device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTensor& t, const AdamwStep& st, int64_t base) {
+  const Quad<FULL, STREAM> io{t.n};
+  float p[kAdamwUnroll][4], g[kAdamwUnroll][4], m[kAdamwUnroll][4], v[kAdamwUnroll][4];
+  float ms[kAdamwUnroll], rs[kAdamwUnroll];
+  uint32_t mc[kAdamwUnroll], rc[kAdamwUnroll];
+#pragma unroll
+  for (int u = 0; u < kAdamwUnroll; ++u) {
+    const int64_t i = base + 1024 * u;
+    if (t.grad_bf16) io.load(g[u], static_cast<const uint16_t*>(t.grad), i);
+    else io.load(g[u], static_cast<const float*>(t.grad), i);
+    if (t.master) io.load(p[u], t.master, i);
+    else if (t.param_bf16) io.load(p[u], static_cast<const uint16_t*>(t.param), i);
+    else io.load(p[u], static_cast<const float*>(t.param), i);
+    if (EIGHT) {
+      mc[u] = io.load_codes(t.avg, i);
+      rc[u] = io.load_codes(t.sq, i);
+      ms[u] = FULL || i < t.n ? t.avg_scales[i / kGroup] : 0.0f;
+      rs[u] = FULL || i < t.n ? t.root_scales[i / kGroup] : 0.0f;
+    } else {
+      io.load(m[u], static_cast<const float*>(t.avg), i);
+      io.load(v[u], static_cast<const float*>(t.sq), i);
+    }
+  }
 #pragma unroll
   for (int u = 0; u < kAdamwUnroll; ++u) {
     const int64_t i = base + 1024 * u;
@@ -170,69 +218,64 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
         v[u][j] = r * r;
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float gv = g[u][j] * gs;
-      m[u][j] = m[u][j] * a.beta1 + gv * a.rest1;
-      v[u][j] = v[u][j] * a.beta2 + (gv * gv) * a.rest2;
-      const float move = (m[u][j] * u1) / (__builtin_sqrtf(v[u][j] * u2) + a.eps);
-      p[u][j] -= lr * (move + t.decay * p[u][j]);
-    }
-    if (t.master) store4(t.master, p[u], i, t.n);
-    if (t.param_bf16) {
-      uint16_t* const dst = static_cast<uint16_t*>(t.param) + i;
-      const uint2 w = make_uint2(pack_bf16(p[u][0], p[u][1]), pack_bf16(p[u][2], p[u][3]));
-      if (i + 4 <= t.n) {
-        *reinterpret_cast<uint2*>(dst) = w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < t.n) dst[j] = (uint16_t)((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
-      }
-    } else {
-      store4(static_cast<float*>(t.param), p[u], i, t.n);
-    }
-    if (!EIGHT) {
-      store4(static_cast<float*>(t.avg), m[u], i, t.n);
-      store4(static_cast<float*>(t.sq), v[u], i, t.n);
-      continue;
-    }
-    // elements past the end are zero here: their gradient and codes were read as zero
     float r[4], mt = 0.0f, rt = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      r[j] = __builtin_sqrtf(v[u][j]);
+      const float gv = g[u][j] * st.grad_scale;
+      m[u][j] = m[u][j] * a.beta1 + gv * a.rest1;
+      v[u][j] = v[u][j] * a.beta2 + (gv * gv) * a.rest2;
+      r[j] = sqrt_rn(v[u][j]);
+      // the quotient by v_rcp_f32: one ulp more than a division, of lr times a number near 1
+      const float move = (m[u][j] * st.unbias1) * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], st.root2, a.eps));
+      p[u][j] -= st.lr * (move + t.decay * p[u][j]);
       mt = fmaxf(mt, fabsf(m[u][j]));
       rt = fmaxf(rt, r[j]);
     }
+    if (t.master) io.store(t.master, p[u], i);
+    if (t.param_bf16) io.store(static_cast<uint16_t*>(t.param), p[u], i);
+    else io.store(static_cast<float*>(t.param), p[u], i);
+    if (!EIGHT) {
+      io.store(static_cast<float*>(t.avg), m[u], i);
+      io.store(static_cast<float*>(t.sq), v[u], i);
+      continue;
+    }
+    // elements past the end are zero here: their gradient and codes were read as zero
     const F32Scale mg = f32_scale(max32_f32(mt)), rg = f32_scale(max32_f32(rt));
-    float mq[4], rq[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mq[j] = f32_quotient<true>(m[u][j], mg);
-      const uint32_t bits = mix32(key + (uint32_t)(i + j) * 0x9E3779B1u) >> 12;
-      const float q = round_at_random(f32_quotient<true>(r[j], rg), bits);
-      rq[j] = r[j] > 0.0f ? fmaxf(q, 0x1p-9f) : 0.0f;
-    }
-    const uint32_t mw = code4_f32(mq[0], mq[1], mq[2], mq[3]), rw = code4_f32(rq[0], rq[1], rq[2], rq[3]);
-    uint8_t* const md = static_cast<uint8_t*>(t.avg) + i;
-    uint8_t* const rd = static_cast<uint8_t*>(t.sq) + i;
-    if (i + 4 <= t.n) {
-      *reinterpret_cast<uint32_t*>(md) = mw;
-      *reinterpret_cast<uint32_t*>(rd) = rw;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < t.n) {
-          md[j] = (uint8_t)(mw >> (8 * j));
-          rd[j] = (uint8_t)(rw >> (8 * j));
-        }
-    }
-    if ((threadIdx.x & 31) == 0 && i < t.n) {
+    const uint32_t random = st.key + (uint32_t)i * 0x9E3779B1u;
+    const bool slow = __ballot(fmaxf(mg.up, rg.up) != 1.0f) != 0;
+    const uint2 w = slow ? state_codes<true>(m[u], r, mg, rg, random) : state_codes<false>(m[u], r, mg, rg, random);
+    io.store_codes(t.avg, w.x, i);
+    io.store_codes(t.sq, w.y, i);
+    if ((threadIdx.x & 31) == 0 && (FULL || i < t.n)) {
       t.avg_scales[i / kGroup] = mg.s;
       t.root_scales[i / kGroup] = rg.s;
     }
   }
+}
+
+template <bool EIGHT, bool STREAM>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
+  // the workgroup's tensor: the last whose first workgroup is not past this one
+  int k = 0;
+  for (int hi = a.count; hi - k > 1;) {
+    const int mid = (k + hi) >> 1;
+    if (a.block0[mid] <= blockIdx.x) k = mid; else hi = mid;
+  }
+  const AdamwTensor& t = a.t[k];
+  AdamwStep st{a.lr, a.grad_scale, a.unbias1, a.root2, 0};
+  uint32_t step = a.step;
+  if (a.scalars) {
+    st.lr = a.scalars[0];
+    st.grad_scale = a.scalars[1];
+    const float n = a.scalars[2];
+    step = (uint32_t)n;
+    st.unbias1 = -1.0f / expm1f(n * a.log1);
+    st.root2 = __builtin_sqrtf(-1.0f / expm1f(n * a.log2));
+  }
+  if (EIGHT) st.key = mix32(mix32(a.seed + step * 0x9E3779B1u) + (a.number + (uint32_t)k) * 0x3C6EF373u);
+  const int64_t first = (int64_t)(blockIdx.x - a.block0[k]) * kAdamwBlock;
+  if (first + kAdamwBlock <= t.n) adamw_block<EIGHT, true, STREAM>(a, t, st, first + 4 * threadIdx.x);
+  else adamw_block<EIGHT, false, STREAM>(a, t, st, first + 4 * threadIdx.x);
 }
 
 }  // namespace fp8bs
@@ -269,7 +312,7 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
   a.log2 = (float)log(beta2);
   if (!scalars) {
     a.unbias1 = (float)(1.0 / (1.0 - pow(beta1, (double)step)));
-    a.unbias2 = (float)(1.0 / (1.0 - pow(beta2, (double)step)));
+    a.root2 = (float)sqrt(1.0 / (1.0 - pow(beta2, (double)step)));
   }
   a.seed = seed;
   a.step = (uint32_t)step;
@@ -282,7 +325,7 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
       continue;
     }
     const bool eight = tensors[i].avg_scales != nullptr;
-    int64_t blocks = 0;
+    int64_t blocks = 0, bytes = 0;
     a.count = 0;
     a.number = (uint32_t)i;
     while (i < num_tensors && a.count < kPerLaunch && tensors[i].n > 0 && (tensors[i].avg_scales != nullptr) == eight) {
@@ -296,9 +339,15 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
                                  (uint16_t)t.param_bf16, (uint16_t)t.grad_bf16};
       a.block0[a.count++] = (uint32_t)blocks;
       blocks += more;
+      bytes += t.n * ((t.grad_bf16 ? 2 : 4) + (t.master ? 6 : t.param_bf16 ? 2 : 4) + (eight ? 2 : 8));
     }
-    if (eight) hipLaunchKernelGGL((adamw_kernel<true>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL((adamw_kernel<false>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+    const dim3 grid((unsigned)blocks), block(256);
+    hipStream_t s = (hipStream_t)stream;
+    const bool large = bytes > kStreamBytes;
+    if (eight && large) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, s, a);
+    else if (eight) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, s, a);
+    else if (large) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, s, a);
     const int st = launch_status();
     if (st != FP8BS_OK) return st;
   }
