@@ -740,17 +740,20 @@ def _codes(q, scales, rows, cols, dev, names):
 
 
 def _code_outputs(q, scales, rows, cols, on, dev, stream, names):
-    """(q, scales, their addresses as _codes gives them) of an optional coded output: q False leaves it out, None
+    """(q, scales, code address, row stride, scale address) of an optional coded output: q False leaves it out, None
     allocates it, a tensor is written; scales None allocates them."""
     if q is False:
         if scales is not None:
             raise ValueError(f"{names[1]} goes with {names[0]}")
-        return None, None, (None, 0, None)
-    if q is None:
-        q = _empty((rows, cols), _u8, on, stream)
+        return None, None, None, 0, None
     if scales is None:
         scales = _empty((rows, cols // GROUP), _f32, on, stream)
-    return q, scales, _codes(q, scales, rows, cols, dev, names)
+        if q is None:                             # both fresh: nothing to check
+            q = _empty((rows, cols), _u8, on, stream)
+            return q, scales, q.data_ptr(), cols, scales.data_ptr()
+    if q is None:
+        q = _empty((rows, cols), _u8, on, stream)
+    return (q, scales, *_codes(q, scales, rows, cols, dev, names))
 
 
 def _rows_output(t, rows, cols, on, dev, stream, name):
@@ -759,15 +762,24 @@ def _rows_output(t, rows, cols, on, dev, stream, name):
         return None, None, 0
     if t is None:
         t = _empty((rows, cols), _bf16, on, stream)
+        return t, t.data_ptr(), cols
     return (t, *_matrix(t, rows, cols, dev, name))
 
 
-def _workspace(workspace, need, on, dev, stream):
-    """(address, bytes, the tensor to keep until the call has been made)"""
-    if workspace is None and need:
-        workspace = _empty(need // 4, _f32, on, stream)
+def _workspace(workspace, coded, size, sizes, on, dev, stream):
+    """(address, bytes, the tensor to keep until the call has been made): the caller's, or, where codes are made, one
+    of size(*sizes) bytes on that device."""
     if workspace is None:
-        return None, 0, None
+        if not coded:
+            return None, 0, None
+        if _current_device() == dev:
+            need = size(*sizes)
+        else:
+            with torch.cuda.device(dev):
+                need = size(*sizes)
+        if need <= 0:                             # none, or sizes that the call itself refuses
+            return None, 0, None
+        workspace = _empty(need // 4, _f32, on, stream)
     return _dense(workspace, _f32, dev, "workspace"), 4 * workspace.numel(), workspace
 
 
@@ -807,12 +819,9 @@ def fp8bs_gemm_gated(qa, sa, qb, sb, act=FP8BS_ACT_SILU, z=None, h=None, qh=Fals
     n, on = rows // 2, qa.device
     pz, ldz = (None, 0) if z is None else _matrix(z, m, 2 * n, dev, "z")
     h, ph, ldh = _rows_output(h, m, n, on, dev, stream, "h")
-    qh, sh, (pqh, ldqh, psh) = _code_outputs(qh, sh, m, n, on, dev, stream, ("qh", "sh"))
-    need = 0
-    if pqh is not None and workspace is None:
-        with torch.cuda.device(dev):
-            need = fp8bs_gemm_gated_workspace(m, n, k)
-    pws, ws_bytes, workspace = _workspace(workspace, need, on, dev, stream)
+    qh, sh, pqh, ldqh, psh = _code_outputs(qh, sh, m, n, on, dev, stream, ("qh", "sh"))
+    pws, ws_bytes, workspace = _workspace(workspace, pqh is not None, raw.fp8bs_gemm_gated_workspace, (m, n, k), on, dev,
+                                          stream)
     _call(raw.fp8bs_gemm_gated, dev, stream, pqa, psa, pqb, psb, m, n, k, act, pz, ldz, ph, ldh, pqh, ldqh, psh, pws,
           ws_bytes)
     return h, qh, sh
@@ -837,12 +846,9 @@ def fp8bs_grouped_gemm_gated_ragged(qa, sa, seg_offsets, qb, sb, act=FP8BS_ACT_S
     n, on = b_rows // 2, qa.device
     pz, ldz = (None, 0) if z is None else _matrix(z, rows, 2 * n, dev, "z")
     h, ph, ldh = _rows_output(h, rows, n, on, dev, stream, "h")
-    qh, sh, (pqh, ldqh, psh) = _code_outputs(qh, sh, rows, n, on, dev, stream, ("qh", "sh"))
-    need = 0
-    if pqh is not None and workspace is None:
-        with torch.cuda.device(dev):
-            need = fp8bs_grouped_gemm_gated_ragged_workspace(num_e, rows, n, k)
-    pws, ws_bytes, workspace = _workspace(workspace, need, on, dev, stream)
+    qh, sh, pqh, ldqh, psh = _code_outputs(qh, sh, rows, n, on, dev, stream, ("qh", "sh"))
+    pws, ws_bytes, workspace = _workspace(workspace, pqh is not None, raw.fp8bs_grouped_gemm_gated_ragged_workspace,
+                                          (num_e, rows, n, k), on, dev, stream)
     _call(raw.fp8bs_grouped_gemm_gated_ragged, dev, stream, pqa, psa, pseg, num_e, rows, pqb, psb, n, k, act, pz, ldz, ph,
           ldh, pqh, ldqh, psh, pws, ws_bytes)
     return h, qh, sh
@@ -866,9 +872,9 @@ def fp8bs_gated_backward(dh, z, act=FP8BS_ACT_SILU, dz=None, q=False, scales=Non
     pz, ldz = _matrix(z, m, 2 * n, dev, "z")
     dz, pdz, lddz = _rows_output(dz, m, 2 * n, on, dev, stream, "dz")
     h, ph, ldh = _rows_output(h, m, n, on, dev, stream, "h")
-    q, scales, (pq, ldq, ps) = _code_outputs(q, scales, m, 2 * n, on, dev, stream, ("q", "scales"))
-    qt, scales_t, (pqt, ldqt, pst) = _code_outputs(qt, scales_t, 2 * n, m, on, dev, stream, ("qt", "scales_t"))
-    qht, scales_ht, (pqht, ldqht, psht) = _code_outputs(qht, scales_ht, n, m, on, dev, stream, ("qht", "scales_ht"))
+    q, scales, pq, ldq, ps = _code_outputs(q, scales, m, 2 * n, on, dev, stream, ("q", "scales"))
+    qt, scales_t, pqt, ldqt, pst = _code_outputs(qt, scales_t, 2 * n, m, on, dev, stream, ("qt", "scales_t"))
+    qht, scales_ht, pqht, ldqht, psht = _code_outputs(qht, scales_ht, n, m, on, dev, stream, ("qht", "scales_ht"))
     pend = None
     if row_end is not None:
         pend = _dense(row_end, _i32, dev, "row_end")
