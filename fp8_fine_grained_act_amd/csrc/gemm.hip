@@ -1694,14 +1694,18 @@ int gated_tile_cols(const GatedArgs& a, int64_t cus) {
   const double high = owners > 1 ? mean + 2.0 * sqrt(mean) : mean;
   const double full = floor(high / 128.0), rest = high - 128.0 * full;
   const double chip = (double)cus;
+  // codes of h made in a launch of their own: 2.5 us and 9 bytes per element at 5 TB/s, in the same unit (2500
+  // rows of n 1792, k 1280 30.1 / 26.8 us on 128 / 256, without codes 23.5 / 24.5)
+  const double pass = a.qh ? (2.5 + 1.8e-6 * (double)p.m * (double)p.n) * 56.0 * 128.0 / (double)p.k : 0.0;
   int best = 0;
-  double best_cost = (double)skinny_cost(p, 0, cus);
+  double best_cost = (double)skinny_cost(p, 0, cus) + pass;
   for (int bn = 128; bn <= 256; bn += 128) {
     const double strips = (double)owners * (double)(p.n / (bn / 2));
     const double one = gated_tile_cost(full > 0 ? 128.0 : rest, bn);
     const double all = full * gated_tile_cost(128.0, bn) + (rest > 0 ? gated_tile_cost(rest, bn) : 0.0);
     const double cost = p.seg ? fmax(one, strips * all / chip) : one * ceil(strips * (full + (rest > 0 ? 1.0 : 0.0)) / chip);
-    if (cost < best_cost) best = bn, best_cost = cost;
+    const double whole = cost + (bn == 256 ? 0.0 : pass);
+    if (whole < best_cost) best = bn, best_cost = whole;
   }
   return best;
 }

@@ -565,6 +565,7 @@ int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const uint16_t* 
  *       each); may be NULL where that is 0 or qh is NULL
  *   n is the width of h.  m >= 1 (any), n % 128 == 0, k % 128 == 0, 2 n k < 2^32,
  *   256 k < 2^32 - 1, m (n / 16) < 2^31; h or qh is needed.  The outputs must not overlap each other or an input.
+ * The bits depend on the sizes and on whether qh is asked for (the kernel is chosen by them), on one kind of device.
  * Alignment: qa, qb, z, h, qh 16 bytes, ldz and ldh % 8 == 0, ldqh % 16 == 0, sa, sb, sh
  * 4 bytes.  Never allocates.  Errors: FP8BS_ERR_SCRATCH when the workspace is missing or too small.
  */

@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+from tests.gated_rules import kernel
 from tests.gated_util import E4M3, backward64, check_codes, gated64
 from tests.linear_util import ACTS, blocks, check, gen, normal, row_tiles
 
@@ -41,6 +42,7 @@ SIZES = [
     (1, 128, 128, "silu"), (4, 2048, 2048, "silu"), (17, 256, 384, "gelu_tanh"), (33, 384, 1280, "relu"), (130, 128, 128, "none"),
     (64, 640, 512, "silu"), (300, 640, 512, "gelu_tanh"), (1037, 1408, 1024, "gelu_tanh"), (2500, 256, 256, "silu"),
     (129, 1280, 1920, "relu"), (3000, 1152, 384, "silu"), (4099, 1024, 128, "none"),
+    (32, 4096, 256, "silu"), (300, 2048, 4096, "silu"),
 ]
 
 
@@ -61,9 +63,12 @@ def test_forward(gpu_lib, m, n, k, act):
     check(h, h64, eh, "h")
     check_codes(q, s, h64, eh, "codes")
     assert untouched(zb, m, 2 * n, NAN) and untouched(hb, m, n, NAN) and untouched(qb, m, n, 0x5A)
-    # the outputs of a call do not depend on which others it makes
+    # the outputs of a call do not depend on which others it makes, but for codes, which can choose another kernel
     only_h, none_q, none_s = gpu_lib.fp8bs_gemm_gated(*dev, act=ACTS[act])
-    assert none_q is None and none_s is None and torch.equal(only_h.view(torch.int16), h.contiguous().view(torch.int16))
+    assert none_q is None and none_s is None
+    check(only_h, h64, eh, "h alone")
+    if kernel(m, n, k, False) == kernel(m, n, k, True):
+        assert torch.equal(only_h.view(torch.int16), h.contiguous().view(torch.int16))
     none_h, only_q, only_s = gpu_lib.fp8bs_gemm_gated(*dev, act=ACTS[act], h=False, qh=None)
     assert none_h is None and torch.equal(only_q, q) and torch.equal(only_s, s)
     torch.cuda.synchronize()
@@ -108,6 +113,8 @@ SEGMENTS = [
     ([130, 0, 1, 64, 17], 384, 384, "relu", 5, 9), ([300, 5, 128, 127, 0, 129], 256, 640, "silu", 0, 3),
     ([1000], 128, 256, "none", 3, 1), ([2, 600, 33, 0, 0, 190, 257, 64], 1024, 256, "silu", 1, 70),
     ([0, 0, 0], 128, 128, "silu", 4, 4), ([40] * 30, 640, 128, "gelu_tanh", 0, 0),
+    ([200, 0, 190, 210], 1280, 3200, "silu", 2, 2), ([600, 300, 700], 2048, 256, "silu", 0, 1),
+    ([2, 1, 0, 3] * 25, 512, 512, "gelu_tanh", 0, 0),
 ]
 
 
@@ -137,7 +144,13 @@ def test_segments(gpu_lib, lengths, n, k, act, lead, tail):
     assert untouched(zb, rows, 2 * n, NAN) and untouched(hb, rows, n, NAN) and untouched(cb, rows, n, 0x5A)
     only_h = torch.full((rows, n), NAN, dtype=torch.bfloat16, device="cuda")
     gpu_lib.fp8bs_grouped_gemm_gated_ragged(*dev, act=ACTS[act], h=only_h)
-    assert torch.equal(only_h.view(torch.int16), h.contiguous().view(torch.int16))
+    for e in range(len(lengths)):
+        cut = slice(int(seg[e]), int(seg[e + 1]))
+        if lengths[e]:
+            check(only_h[cut], *gated64(qa[cut], sa[cut], qb[e], sb[e], act)[2:], f"h alone of expert {e}")
+    assert only_h[out.cuda()].isnan().all()
+    if kernel(rows, n, k, False, len(lengths)) == kernel(rows, n, k, True, len(lengths)):
+        assert torch.equal(only_h.view(torch.int16), h.contiguous().view(torch.int16))
 
 
 def test_segments_that_hold_bad_offsets(gpu_lib):
