@@ -175,7 +175,11 @@ __device__ __forceinline__ uint2 state_codes(const float (&m)[4], const float (&
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     mq[j] = f32_quotient<SLOW>(m[j], mg);
-    const float q = fminf(f32_quotient<SLOW>(r[j], rg), kE4M3Max);
+    // rounding upwards with the probability of q's place needs q cut off, not rounded: one unit less where
+    // its remainder is negative (-0.5 of the bits' 2^-20 on average otherwise, all upwards)
+    float q = fminf(f32_quotient<SLOW>(r[j], rg), kE4M3Max);
+    const float left = __builtin_fmaf(-q, rg.s * rg.up, r[j] * rg.up);
+    q = __int_as_float(__float_as_int(q) + (__float_as_int(left) >> 31));
     rq[j] = fmaxf(round_at_random(q, mix32(random + (uint32_t)j * 0x9E3779B1u) >> 12), r[j] > 0.0f ? 0x1p-9f : 0.0f);
   }
   return make_uint2(code4_f32(mq[0], mq[1], mq[2], mq[3]), code4_f32(rq[0], rq[1], rq[2], rq[3]));

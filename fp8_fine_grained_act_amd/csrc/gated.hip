@@ -152,6 +152,17 @@ __global__ __launch_bounds__(256) void gated_bwd_rows_kernel(GatedBwdArgs p, uin
   }
 }
 
+// The square (column, row) of workgroup b.  Each XCD (they take workgroups in turn) owns one
+// range of squares, in bands of 8 squares down: neighbours in both directions then
+// meet in one L2, and with them the scales' lines, of which a square writes 4 bytes,
+// and the transposed rows' pages (16384 x 2048 82 -> 79 us, 8192 x 7168 139 -> 125; bands of 1 128, of 32 131).
+__device__ __forceinline__ uint2 square_of(uint32_t b, uint32_t nx, uint32_t ny) {
+  const uint32_t per = (nx * ny + 7) / 8, full = nx * ny - 8 * (per - 1), x = b % 8, j = b / 8;
+  const uint32_t l = x < full ? x * per + j : full * per + (x - full) * (per - 1) + j;
+  const uint32_t band = l / (8 * nx), r = l - band * 8 * nx, rows = min(8u, ny - 8 * band);
+  return make_uint2(r / rows, 8 * band + r % rows);
+}
+
 // With transposed outputs: a workgroup of 8 waves owns a square of 128 rows and 128
 // columns of h.  Thread (cg, rg) = (tid % 16, tid / 16) holds columns 8 cg .. 8 cg + 7 of rows
 // 4 rg .. 4 rg + 3 in FP32 registers, so both tile directions are coded from the
@@ -168,7 +179,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
   __shared__ __attribute__((aligned(16))) uint32_t codes[3][128 * 32];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid & 15, rg = tid >> 4;
-  const int64_t c0 = (int64_t)blockIdx.x * 128, r0 = (int64_t)blockIdx.y * 128;
+  const uint2 square = square_of(blockIdx.x, (uint32_t)(p.n / kGroup), (uint32_t)(p.m / kGroup));
+  const uint32_t bx = square.x, by = square.y;
+  const int64_t c0 = (int64_t)bx * 128, r0 = (int64_t)by * 128;
   const int64_t col = c0 + 8 * cg;
   const int nq = p.qht ? 3 : 2, q0 = p.qt ? 0 : 2;
   auto load = [](const uint16_t* a) { return STREAM ? load_nt(a) : *reinterpret_cast<const uint4*>(a); };
@@ -192,7 +205,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
     if (p.h) *reinterpret_cast<uint4*>(p.h + row * p.ldh + col) = pack8(x[2][i]);
     if (p.q) {
       uint8_t* const qr = p.q + row * p.ldq + col;
-      float* const sr = p.s + row * (2 * p.n / kGroup) + blockIdx.x;
+      float* const sr = p.s + row * (2 * p.n / kGroup) + bx;
       store_row_codes(x[0][i], x[1][i], qr, qr + p.n, sr, sr + p.n / kGroup, cg);
     }
     __builtin_amdgcn_sched_barrier(0);         // a row at a time: few live temporaries
@@ -225,7 +238,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
     if (g.up != 1.0f) tiny = 1;
     if (q >= q0 && q < nq) {
       float* const s = q == 2 ? p.sht : p.st + (q * p.n) * (p.m / kGroup);
-      s[(c0 + c) * (p.m / kGroup) + blockIdx.y] = g.s;
+      s[(c0 + c) * (p.m / kGroup) + by] = g.s;
     }
   }
   __syncthreads();
@@ -266,7 +279,7 @@ template <int ACT>
 static int launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s) {
   const bool stream = 6 * a.m * a.n > kStreamBytes;
   if (a.qt || a.qht) {
-    const dim3 grid((unsigned)(a.n / kGroup), (unsigned)(a.m / kGroup));
+    const dim3 grid((unsigned)((a.n / kGroup) * (a.m / kGroup)));
     if (stream) hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, true>), grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, false>), grid, dim3(512), 0, s, a);
     return launch_status();
@@ -282,16 +295,13 @@ static int launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s) {
 
 using namespace fp8bs;
 
-static bool fits_u32(int64_t bytes) { return bytes < 0xFFFFFFFFLL; }
-
 // Checks shared by the two forward entry points (m, n, k known to be non-negative).
 static int gated_check(const GatedArgs& a, float* workspace) {
   const SkinnyArgs& p = a.p;
   if ((a.qh == nullptr) != (a.sh == nullptr) || (p.m > 0 && !p.c && !a.qh)) return FP8BS_ERR_NULL;
   if (p.epi.act < FP8BS_ACT_NONE || p.epi.act > FP8BS_ACT_SILU) return FP8BS_ERR_FLAG;
   if (p.n <= 0 || p.k <= 0 || p.n % 128 || p.k % BK || (p.c && p.ldc < p.n) || (p.epi.z && p.epi.ldz < 2 * p.n) ||
-      (a.qh && a.ldqh < p.n) || p.n > 0x3FFFFFFFLL || !fits_u32(256 * p.k) || p.n > 0xFFFFFFFFLL / (2 * p.k) ||
-      p.m > kMaxGrid / (p.n / 16))
+      (a.qh && a.ldqh < p.n) || p.k >= 1 << 24 || p.n > 0xFFFFFFFFLL / (2 * p.k) || p.m > kMaxGrid / (p.n / 16))
     return FP8BS_ERR_SHAPE;
   if (!aligned(p.qa, 16) || !aligned(p.qb, 16) || !aligned(p.sa, 4) || !aligned(p.sb, 4) || !aligned(p.seg, 4) ||
       (p.c && (!aligned(p.c, 16) || p.ldc % 8)) || (p.epi.z && (!aligned(p.epi.z, 16) || p.epi.ldz % 8)) ||
@@ -370,12 +380,12 @@ extern "C" int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint
                                     int act, uint16_t* dz, int64_t lddz, uint8_t* q, int64_t ldq, float* scales, uint8_t* qt,
                                     int64_t ldqt, float* scales_t, uint16_t* h, int64_t ldh, uint8_t* qht, int64_t ldqht,
                                     float* scales_ht, const int32_t* row_end, void* stream) {
-  if (!dh || !z || (!dz && !q && !qt && !h && !qht) || (q == nullptr) != (scales == nullptr) ||
+  if ((m > 0 && (!dh || !z || (!dz && !q && !qt && !h && !qht))) || (q == nullptr) != (scales == nullptr) ||
       (qt == nullptr) != (scales_t == nullptr) || (qht == nullptr) != (scales_ht == nullptr))
     return FP8BS_ERR_NULL;
   if (act < FP8BS_ACT_NONE || act > FP8BS_ACT_SILU) return FP8BS_ERR_FLAG;
   const bool cols = qt || qht;
-  if (m <= 0 || n <= 0 || n % 8 || n > 0x3FFFFFFFLL || m > 0x7FFFFFFFLL || ((q || cols) && n % kGroup) ||
+  if (m < 0 || n <= 0 || n % 8 || n > 0x3FFFFFFFLL || m > 0x7FFFFFFFLL || ((q || cols) && n % kGroup) ||
       (cols && (m % kGroup || row_end || m / kGroup > 65535)) || m > kMaxGrid / ((n + kGroup - 1) / kGroup) - 16 || lddh < n ||
       ldz < 2 * n || (dz && lddz < 2 * n) || (q && ldq < 2 * n) || (qt && ldqt < m) || (h && ldh < n) || (qht && ldqht < m))
     return FP8BS_ERR_SHAPE;
@@ -384,6 +394,7 @@ extern "C" int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint
       (qht && (!aligned(qht, 16) || ldqht % 16)) || !aligned(scales, 4) || !aligned(scales_t, 4) || !aligned(scales_ht, 4) ||
       !aligned(row_end, 4))
     return FP8BS_ERR_ALIGN;
+  if (m == 0) return FP8BS_OK;
   const GatedBwdArgs a{dh, lddh, z, ldz, m, n, dz, lddz, q, ldq, scales, qt, ldqt, scales_t, h, ldh, qht, ldqht, scales_ht, row_end};
   hipStream_t s = (hipStream_t)stream;
   switch (act) {

@@ -559,12 +559,12 @@ int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const uint16_t* 
  *   h   bf16 [m, n], row stride ldh, or NULL: h rounded once
  *   qh, sh  E4M3 [m, n], row stride ldqh bytes, and f32 [m, n/128], or both NULL: the 1x128
  *       tiles of the unrounded h along the columns, the down projection's input (s =
- *       amax / 448, codes of the quotient as fp8bs_quantize_act_1x128 takes it)
+ *       amax / 448, codes to nearest even of h / s)
  *   workspace  16-byte aligned, at least fp8bs_gemm_gated_workspace(m, n, k) bytes, used only by
  *       this call until it has run (two captured graphs that may run at once need one
  *       each); may be NULL where that is 0 or qh is NULL
- *   n is the width of h.  m >= 1 (any), n % 128 == 0, k % 128 == 0, 2 n k < 2^32,
- *   256 k < 2^32 - 1, m (n / 16) < 2^31; h or qh is needed.  The outputs must not overlap each other or an input.
+ *   n is the width of h.  m >= 1 (any), n % 128 == 0, k % 128 == 0, k < 2^24, 2 n k < 2^32,
+ *   m (n / 16) < 2^31; h or qh is needed.  The outputs must not overlap each other or an input.
  * The bits depend on the sizes and on whether qh is asked for (the kernel is chosen by them), on one kind of device.
  * Alignment: qa, qb, z, h, qh 16 bytes, ldz and ldh % 8 == 0, ldqh % 16 == 0, sa, sb, sh
  * 4 bytes.  Never allocates.  Errors: FP8BS_ERR_SCRATCH when the workspace is missing or too small.
@@ -601,7 +601,8 @@ int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t t
  *   qht, scales_ht E4M3 [n, m], row stride ldqht, f32 [n, m/128]: the same of h (weight gradients: fp8bs_gemm_wgrad)
  *   row_end  int32 on the device, or NULL: rows from *row_end on are neither read nor written (the end of the
  *            last expert segment, seg_offsets + num_experts)
- * Codes are those of the unrounded FP32 values.  m >= 1, n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
+ * Codes are the nearest to x / s of the unrounded FP32 values x (the quotient within two units in its last place).
+ * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
  * m % 128 == 0 and row_end NULL, m < 2^23.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an input, but dz may be z (same
  * pointer and stride) where neither qt nor qht is asked for, and h may be dh.
  * Alignment: bf16 and code pointers 16 bytes, bf16 strides % 8 == 0, code strides % 16 == 0, scales and row_end 4 bytes.

@@ -172,6 +172,8 @@ def test_no_rows(gpu_lib):
         torch.empty((0, k), dtype=torch.uint8, device="cuda"), torch.empty((0, k // 128), device="cuda"),
         torch.zeros(4, dtype=torch.int32, device="cuda"), qb.cuda(), sb.cuda(), qh=None)
     assert h.shape == (0, n) and q.shape == (0, n) and s.shape == (0, n // 128)
+    got = gpu_lib.fp8bs_gated_backward(h, torch.empty((0, 2 * n), dtype=torch.bfloat16, device="cuda"), q=None, h=None)
+    assert got[0].shape == (0, 2 * n) and got[1].shape == (0, 2 * n) and got[5].shape == (0, n)
 
 
 def test_bindings_refusals(gpu_lib):
@@ -191,9 +193,10 @@ def test_bindings_refusals(gpu_lib):
         gpu_lib.fp8bs_gemm_gated(*dev, sh=torch.empty((4, 1), device="cuda"))
     with pytest.raises(ValueError):
         gpu_lib.fp8bs_gemm_gated(*dev, qh=torch.empty((4, 64), dtype=torch.uint8, device="cuda"))
-    if gpu_lib.fp8bs_gemm_gated_workspace(4, 128, 256):
-        with pytest.raises(gpu_lib.Fp8bsError):
-            gpu_lib.fp8bs_gemm_gated(*dev, qh=None, workspace=torch.empty(4, device="cuda"))
+    long = [t.cuda() for t in operands(g, 4, 128, 7168)]
+    assert gpu_lib.fp8bs_gemm_gated_workspace(4, 128, 7168) == 4 * 4 * 128
+    with pytest.raises(gpu_lib.Fp8bsError):
+        gpu_lib.fp8bs_gemm_gated(*long, qh=None, workspace=torch.empty(4, device="cuda"))
     dh, z = torch.zeros((128, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((128, 256), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):
         gpu_lib.fp8bs_gated_backward(dh, z[:, :128])
