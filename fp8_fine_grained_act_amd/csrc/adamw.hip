@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include "common.h"
+#include "f32_codes.h"
 #include "launch.h"
 
 namespace fp8bs {

@@ -7,11 +7,16 @@
 // backward pass read is made in the same pass, from the unrounded FP32 values: the
 // 1x128 tiles of dz = [dg, du] along the columns (activation gradient), and along the
 // rows, transposed (weight gradients of both weights; h's for the down projection).
-// Bound by HBM: 6 bytes read per element of h, 2 to 10 written.
+// Bound by HBM: 6 bytes read per element of h, 2 to 10 written.  Without transposed outputs
+// 32768 x 2048 in 140 us with dz, h and codes (6.7 TB/s), 16384 x 2048 with codes alone in 43
+// us (6.3 TB/s); with both orientations and h's, 16384 x 2048 in 79-81 us (4.7 TB/s), where the
+// arithmetic (31 VALU instructions per element, 34 us of issue) and the phases between
+// barriers of only two squares per CU come on top.
 
 #include <type_traits>
 
 #include "common.h"
+#include "f32_codes.h"
 #include "gated.h"
 #include "launch.h"
 
@@ -19,7 +24,8 @@ namespace fp8bs {
 
 // ---- codes of h from its FP32 values -----------------------------------------------
 // h [m, n] FP32 contiguous -> 1x128 tiles along the columns.  16 lanes per tile, 8 values each.  With
-// seg only the rows of segments (between the first offset and the last).
+// seg only the rows of segments (between the first offset and the last).  A launch of its
+// own, 2 us for a few rows, 8 us (4.7 TB/s) for 4096 x 2048.
 __global__ __launch_bounds__(256) void quant_h_kernel(const float* __restrict__ hf, int64_t m, int64_t n,
                                                       const int32_t* __restrict__ seg, int64_t num_experts,
                                                       uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
@@ -171,6 +177,8 @@ __device__ __forceinline__ uint2 square_of(uint32_t b, uint32_t nx, uint32_t ny)
 // codes, 4 bytes of a column per thread, meet in LDS and leave as whole 128-byte
 // rows of the output: dword d of column c is stored at d ^ (4 * ((c / 8) % 8)), which
 // keeps 16-byte chunks whole and puts a wave's 64 writes on 32 banks, two each.
+// 128 registers (the FP32 values are 96 of them), so that two squares share a CU: 140 us
+// for 16384 x 2048 with 136 registers and one, 86 with two.
 template <int ACT, bool STREAM>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_square_kernel(GatedBwdArgs p) {
   __shared__ float tops[3][8][128];            // [dg, du, h][wave][column]

@@ -16,10 +16,10 @@
 // tiles, every wave both copies and multiplies, two workgroups per CU; small
 // problems, and the grouped GEMM whose n is not a multiple of 256) and
 // gemm_ws_kernel (256 x 128, 192 x 128, 128 x 192
-// and, for the MoE grouped GEMM, 128 x 256 tiles; separate copy and MFMA
-// waves; persistent over tiles where a workgroup gets several; described
+// and, for the MoE grouped GEMM and the gated products, 128 x 256 tiles; separate
+// copy and MFMA waves; persistent over tiles where a workgroup gets several; described
 // above that kernel).  The host picks the kernel, tile shape and tile order
-// (use_ws, tile_cost, choose_group_m).
+// (use_ws, tile_cost, gated_tile_cols, choose_group_m).
 //
 // Structure of one gemm_kernel workgroup (WAVES_M x WAVES_N waves, each wave a
 // (BM/WAVES_M) x (BN/WAVES_N) patch of 16x16 MFMA tiles):
@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "f32_codes.h"
 #include "gated.h"
 #include "launch.h"
 
