@@ -857,7 +857,7 @@ def fp8bs_grouped_gemm_gated_ragged(qa, sa, seg_offsets, qb, sb, act=FP8BS_ACT_S
 def fp8bs_gated_backward(dh, z, act=FP8BS_ACT_SILU, dz=None, q=False, scales=None, qt=False, scales_t=None, h=False,
                          qht=False, scales_ht=None, row_end=None, stream=None):
     """A gated block's backward pass from dh bf16 [m, n] and the kept z = [g, u] bf16 [m, 2n]:
-    dz = [dh u act'(g), dh act(g)] and h = act(g) u.  Returns (dz, q, scales, qt, scales_t, h, qht, scales_ht).
+    dz = [dh u act'(g), dh act(g)] and h = act(g) u (dz may be z itself, h dh).  Returns (dz, q, scales, qt, scales_t, h, qht, scales_ht).
 
     dz, h bf16; q uint8 [m, 2n] and scales f32 [m, 2n/128]: dz's tiles along the columns; qt uint8 [2n, m] and scales_t
     [2n, m/128]: along the rows, transposed; qht [n, m] and scales_ht: the same of h.  Each of dz, q, qt, h, qht: a
@@ -901,7 +901,7 @@ def fp8bs_adamw_table(params, grads, avg, sq, master=None, avg_scales=None, root
     params bf16 or f32; grads f32 or bf16; avg, sq: m and v in f32, or (uint8, with avg_scales and root_scales, f32
     [ceil(n / 128)] each) the codes of m and of sqrt(v); master: f32 copies of bf16 params (a list, entries may be None,
     or None); avg_scales, root_scales: lists (entries None where the states are f32) or None; weight_decay: a number or
-    a list of numbers."""
+    a list of numbers.  What the step writes may not overlap anything else; a gradient may serve several entries."""
     params, grads, avg, sq = list(params), list(grads), list(avg), list(sq)
     count = len(params)
     spread = lambda x: [None] * count if x is None else list(x)  # noqa: E731
@@ -909,7 +909,7 @@ def fp8bs_adamw_table(params, grads, avg, sq, master=None, avg_scales=None, root
     decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
     if not all(len(x) == count for x in (grads, avg, sq, master, avg_scales, root_scales, decay)):
         raise ValueError("the lists must have the same length")
-    entries, kept, dev = (_AdamwTensor * count)(), [], None
+    entries, kept, dev, spans = (_AdamwTensor * count)(), [], None, []
     for i in range(count):
         p, g = params[i], grads[i]
         if dev is None:
@@ -935,7 +935,17 @@ def fp8bs_adamw_table(params, grads, avg, sq, master=None, avg_scales=None, root
         if eight and any(t.numel() != -(-n // GROUP) for t in (avg_scales[i], root_scales[i])):
             raise ValueError(f"avg_scales[{i}] and root_scales[{i}] must have a number for each 128 elements")
         entries[i] = _AdamwTensor(pp, pw, pg, pm, pv, pms, prs, n, decay[i], p.dtype is _bf16, g.dtype is _bf16)
-        kept += [t.detach() for t in (p, g, avg[i], sq[i], master[i], avg_scales[i], root_scales[i]) if t is not None]
+        written = [t for t in (p, avg[i], sq[i], master[i], avg_scales[i], root_scales[i]) if t is not None]
+        spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i, True) for t in written if n]
+        spans += [(g.data_ptr(), g.data_ptr() + n * g.element_size(), i, False)] if n else []
+        kept += [t.detach() for t in (g, *written)]
+    end, writes = 0, False                        # of the memory seen so far, in order of addresses
+    for start, stop, i, write in sorted(spans):
+        if start < end and (write or writes):
+            raise ValueError(f"a tensor of entry {i} overlaps another that the step writes")
+        if start >= end:
+            writes = False
+        end, writes = max(end, stop), writes or write
     return AdamwTable(entries, count, dev, kept)
 
 

@@ -603,8 +603,8 @@ int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t t
  *            last expert segment, seg_offsets + num_experts)
  * Codes are the nearest to x / s of the unrounded FP32 values x (the quotient within two units in its last place).
  * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
- * m % 128 == 0 and row_end NULL, m < 2^23.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an input, but dz may be z (same
- * pointer and stride) where neither qt nor qht is asked for, and h may be dh.
+ * m % 128 == 0 and row_end NULL, m < 2^23.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an
+ * input, but dz may be z and h may be dh (same pointer and stride).
  * Alignment: bf16 and code pointers 16 bytes, bf16 strides % 8 == 0, code strides % 16 == 0, scales and row_end 4 bytes.
  */
 int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int64_t ldz, int64_t m, int64_t n, int act,
@@ -643,7 +643,7 @@ typedef struct fp8bs_adamw_tensor {
  * the table, the element's index), so equal calls give equal bits.
  *   scalars  f32 [3] on the device: lr, grad_scale and step (a whole number from 1 to 2^24), read when the kernels run
  *            and in place of the arguments of these names (a step captured into a graph); or NULL
- * No tensor may overlap another.  0 <= beta < 1, eps >= 0, step >= 1 (else FP8BS_ERR_FLAG).  Never allocates.
+ * No tensor may overlap another, but gradients may be shared.  Gradients and their squares must be finite in FP32.  0 <= beta < 1, eps >= 0, step >= 1 (else FP8BS_ERR_FLAG).  Never allocates.
  * Alignment: param, master, grad, avg, sq 16 bytes, scales and scalars 4 bytes.  FP8BS_ERR_NULL also when exactly one
  * of avg_scales, root_scales is NULL; FP8BS_ERR_FLAG for a master beside an f32 param.  Everything is checked before
  * the first kernel is enqueued.

@@ -132,6 +132,25 @@ def test_views_of_flat_storage(gpu_lib):
     assert torch.equal(flat["g"], before["g"]) and not torch.equal(flat["p"][own], before["p"][own])
 
 
+@pytest.mark.parametrize("n", [1, 126, 127, 129, 1023, 1025, 4001])
+def test_nothing_behind_the_end(gpu_lib, n):
+    """8-bit states, bf16 parameters and gradients in the middle of larger buffers: the rest keeps what it held."""
+    groups = -(-n // 128)
+    make = lambda t, k: torch.full((k + 512,), 3, dtype=t, device="cuda")  # noqa: E731
+    sizes = {"p": (torch.bfloat16, n), "w": (torch.float32, n), "g": (torch.bfloat16, n), "m": (torch.uint8, n),
+             "r": (torch.uint8, n), "ms": (torch.float32, groups), "rs": (torch.float32, groups)}
+    buffers = {k: make(*v) for k, v in sizes.items()}
+    views = {k: buffers[k][256:256 + v[1]] for k, v in sizes.items()}
+    table = gpu_lib.fp8bs_adamw_table([views["p"]], [views["g"]], [views["m"]], [views["r"]], master=[views["w"]],
+                                      avg_scales=[views["ms"]], root_scales=[views["rs"]])
+    gpu_lib.fp8bs_adamw_step(table, 0.5, 1)
+    torch.cuda.synchronize()
+    for k, b in buffers.items():
+        assert (b[:256] == 3).all() and (b[256 + sizes[k][1]:] == 3).all(), k
+        assert k == "g" or not (views[k] == 3).all(), k
+    assert (views["g"] == 3).all()
+
+
 def test_rounding_at_random(gpu_lib):
     """Over many seeds the mean of r's codes nears r: half of 1/sqrt(seeds) of a step, times 6; two seeds differ,
     one seed twice does not."""
@@ -228,6 +247,18 @@ def test_table_refusals(gpu_lib):
         f([x(256)[::2]], [x()], [x()], [x()])
     with pytest.raises(TypeError):
         f([x().cpu()], [x()], [x()], [x()])
+    p, m, big = x(), x(), x(1024)
+    with pytest.raises(ValueError):
+        f([p, p], [x(), x()], [x(), x()], [x(), x()])
+    with pytest.raises(ValueError):
+        f([p], [x()], [m], [m])
+    with pytest.raises(ValueError):
+        f([p], [p], [x()], [x()])
+    with pytest.raises(ValueError):
+        f([big[:512], x()], [x(512), x()], [x(512), big[508:636]], [x(512), x()])
+    g = x()
+    f([p, x()], [g, g], [x(), x()], [m, x()])         # a shared gradient is read twice
+    f([big[:512], big[512:]], [x(512), x(512)], [x(512), x(512)], [x(512), x(512)])
     odd = f([x(256)[1:129]], [x()], [x()], [x()])
     with pytest.raises(gpu_lib.Fp8bsError):
         gpu_lib.fp8bs_adamw_step(odd, 1e-3, 1)

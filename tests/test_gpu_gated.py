@@ -290,6 +290,11 @@ def test_backward_both_orientations(gpu_lib, m, n, act):
     sh2 = torch.full((n, m // 128), NAN, device="cuda")
     gpu_lib.fp8bs_gated_backward(dhd, zd, act=ACTS[act], dz=False, qht=qhv, scales_ht=sh2)
     assert torch.equal(qhv, qht) and torch.equal(sh2, sht) and untouched(hb, n, m, 0x5A)
+    # in place
+    zz, dd = zd.clone(), dhd.clone()
+    again = gpu_lib.fp8bs_gated_backward(dd, zz, act=ACTS[act], dz=zz, q=None, qt=None, h=dd, qht=None)
+    for a, b in zip(again, (dz, q, s, qt, st, h, qht, sht)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
 def test_backward_tiny_and_zero_groups(gpu_lib):
