@@ -49,16 +49,19 @@ __device__ __forceinline__ float max_swap32_f32(float a, float b) {
 struct F32Scale {
   float s, r, rl, up;
 };
-__device__ __forceinline__ float over_448(float amax) {
+__device__ __forceinline__ float over_448_normal(float amax) {   // amax >= 2^-100
   constexpr float kInv = 1.0f / kE4M3Max;
   const float q = amax * kInv;
-  const float s = __builtin_fmaf(__builtin_fmaf(-kE4M3Max, q, amax), kInv, q);
-  return amax < 0x1p-100f ? amax / kE4M3Max : s;
+  return __builtin_fmaf(__builtin_fmaf(-kE4M3Max, q, amax), kInv, q);
 }
+__device__ __forceinline__ float over_448(float amax) {
+  return amax < 0x1p-100f ? amax / kE4M3Max : over_448_normal(amax);
+}
+constexpr float kTinyGroup = 0x1p-64f;         // below: the slow forms
 __device__ __forceinline__ F32Scale f32_scale(float amax) {
   F32Scale g;
   g.s = over_448(amax);
-  g.up = amax < 0x1p-64f ? kTinyScale : 1.0f;
+  g.up = amax < kTinyGroup ? kTinyScale : 1.0f;
   const float d = g.s * g.up;
   g.r = d == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(d);
   g.rl = __builtin_fmaf(-d, g.r, 1.0f) * g.r;
@@ -75,8 +78,9 @@ template <bool SLOW>
 __device__ __forceinline__ float f32_quotient_fast(float x, float r, float up) {
   return SLOW ? __builtin_amdgcn_fmed3f(x * up * r, -kE4M3Max, kE4M3Max) : x * r;
 }
+// The second conversion overwrites the first one's upper half, for which a stands (no register to clear).
 __device__ __forceinline__ uint32_t code4_f32(float a, float b, float c, float d) {
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, __float_as_int(a), false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true);
 }
 

@@ -9,8 +9,8 @@
 // rows, transposed (weight gradients of both weights; h's for the down projection).
 // Bound by HBM: 6 bytes read per element of h, 2 to 10 written.  Without transposed outputs
 // 32768 x 2048 in 140 us with dz, h and codes (6.7 TB/s), 16384 x 2048 with codes alone in 43
-// us (6.3 TB/s); with both orientations and h's, 16384 x 2048 in 79-81 us (4.7 TB/s), where the
-// arithmetic (31 VALU instructions per element, 34 us of issue) and the phases between
+// us (6.3 TB/s); with both orientations and h's, 16384 x 2048 in 76-78 us (4.9 TB/s), where the
+// arithmetic (34 VALU instructions per element, 34 us of issue) and the phases between
 // barriers of only two squares per CU come on top.
 
 #include <type_traits>
@@ -108,24 +108,32 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// 8 codes of one row's tile piece of dg and of du, their scales stored by the tiles' first lane (16 lanes a tile)
+// 8 codes of one row's tile piece of dg and of du, their scales stored by the tiles' first lane (16 lanes a
+// tile).  Where every group of the wave is of ordinary size, a scale takes three operations and its reciprocal one.
 template <bool SLOW>
-__device__ __forceinline__ uint2 row_codes(const float (&x)[8], const F32Scale& g) {
+__device__ __forceinline__ uint2 row_codes(const float (&x)[8], float r, float up) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = f32_quotient_fast<SLOW>(x[i], g.r, g.up);
+  for (int i = 0; i < 8; ++i) v[i] = f32_quotient_fast<SLOW>(x[i], r, up);
   return make_uint2(code4_f32(v[0], v[1], v[2], v[3]), code4_f32(v[4], v[5], v[6], v[7]));
 }
-__device__ __forceinline__ void store_row_codes(const float (&dg)[8], const float (&du)[8], uint8_t* qg, uint8_t* qu,
-                                                float* sg, float* su, int lane16) {
-  const F32Scale a = f32_scale(max16_f32(top8(dg))), b = f32_scale(max16_f32(top8(du)));
-  const bool slow = __ballot(fmaxf(a.up, b.up) != 1.0f) != 0;
-  *reinterpret_cast<uint2*>(qg) = slow ? row_codes<true>(dg, a) : row_codes<false>(dg, a);
-  *reinterpret_cast<uint2*>(qu) = slow ? row_codes<true>(du, b) : row_codes<false>(du, b);
-  if (lane16 == 0) {
-    *sg = a.s;
-    *su = b.s;
+struct RowCodes {
+  uint2 g, u;                // codes of dg and du
+  float sg, su;
+};
+__device__ __forceinline__ RowCodes code_row(const float (&dg)[8], const float (&du)[8]) {
+  const float a = max16_f32(top8(dg)), b = max16_f32(top8(du));
+  RowCodes o;
+  if (__ballot(fminf(a, b) < kTinyGroup)) {
+    const F32Scale ga = f32_scale(a), gb = f32_scale(b);
+    o = RowCodes{row_codes<true>(dg, ga.r, ga.up), row_codes<true>(du, gb.r, gb.up), ga.s, gb.s};
+  } else {
+    o.sg = over_448_normal(a);
+    o.su = over_448_normal(b);
+    o.g = row_codes<false>(dg, __builtin_amdgcn_rcpf(o.sg), 1.0f);
+    o.u = row_codes<false>(du, __builtin_amdgcn_rcpf(o.su), 1.0f);
   }
+  return o;
 }
 
 // Without transposed outputs: 16 lanes per piece of 128 columns of a row.
@@ -154,14 +162,20 @@ __global__ __launch_bounds__(256) void gated_bwd_rows_kernel(GatedBwdArgs p, uin
   if (p.q) {
     uint8_t* const qr = p.q + row * p.ldq + col;
     float* const sr = p.s + row * (int64_t)(2 * pieces_n) + tb;
-    store_row_codes(dg, du, qr, qr + p.n, sr, sr + pieces_n, lane16);
+    const RowCodes o = code_row(dg, du);
+    *reinterpret_cast<uint2*>(qr) = o.g;
+    *reinterpret_cast<uint2*>(qr + p.n) = o.u;
+    if (lane16 == 0) {
+      sr[0] = o.sg;
+      sr[pieces_n] = o.su;
+    }
   }
 }
 
 // The square (column, row) of workgroup b.  Each XCD (they take workgroups in turn) owns one
 // range of squares, in bands of 8 squares down: neighbours in both directions then
 // meet in one L2, and with them the scales' lines, of which a square writes 4 bytes,
-// and the transposed rows' pages (16384 x 2048 82 -> 79 us, 8192 x 7168 139 -> 125; bands of 1 128, of 32 131).
+// and the transposed rows' pages (8192 x 7168 139 -> 125 us; by now 117, with bands of 4 119, of 32 122).
 __device__ __forceinline__ uint2 square_of(uint32_t b, uint32_t nx, uint32_t ny) {
   const uint32_t per = (nx * ny + 7) / 8, full = nx * ny - 8 * (per - 1), x = b % 8, j = b / 8;
   const uint32_t l = x < full ? x * per + j : full * per + (x - full) * (per - 1) + j;
@@ -178,43 +192,64 @@ __device__ __forceinline__ uint2 square_of(uint32_t b, uint32_t nx, uint32_t ny)
 // rows of the output: dword d of column c is stored at d ^ (4 * ((c / 8) % 8)), which
 // keeps 16-byte chunks whole and puts a wave's 64 writes on 32 banks, two each.
 // 128 registers (the FP32 values are 96 of them), so that two squares share a CU: 140 us
-// for 16384 x 2048 with 136 registers and one, 86 with two.
-template <int ACT, bool STREAM>
+// for 16384 x 2048 with 136 registers and one, 86 with two.  An address is the wave's, in
+// scalar registers, plus the lane's 32-bit offset, at most 15 rows away: strides are below
+// 2^28 elements (81 -> 78.5 us, with the ordinary groups' shorter scales).
+constexpr int64_t kMaxSquareStride = (1 << 28) - 1;
+
+template <int ACT, int STREAM>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_square_kernel(GatedBwdArgs p) {
   __shared__ float tops[3][8][128];            // [dg, du, h][wave][column]
   __shared__ float rcps[3][128], ups[3][128];  // a column's r and up
   __shared__ int tiny;                         // some up is not 1
   __shared__ __attribute__((aligned(16))) uint32_t codes[3][128 * 32];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int cg = tid & 15, rg = tid >> 4;
   const uint2 square = square_of(blockIdx.x, (uint32_t)(p.n / kGroup), (uint32_t)(p.m / kGroup));
   const uint32_t bx = square.x, by = square.y;
   const int64_t c0 = (int64_t)bx * 128, r0 = (int64_t)by * 128;
-  const int64_t col = c0 + 8 * cg;
+  const int64_t rw = r0 + 16 * wave;           // the wave's first row
+  const uint32_t r4 = 4 * (rg & 3);            // the lane's first row from there
   const int nq = p.qht ? 3 : 2, q0 = p.qt ? 0 : 2;
   auto load = [](const uint16_t* a) { return STREAM ? load_nt(a) : *reinterpret_cast<const uint4*>(a); };
+  auto store = [](void* a, uint4 v, int from) {  // past the caches from that degree on
+    if (STREAM >= from) store_nt(a, v);
+    else *reinterpret_cast<uint4*>(a) = v;
+  };
   uint4 dhv[4], gv[4], uv[4];
+  {
+    const uint32_t od = r4 * (uint32_t)p.lddh + 8 * cg, oz = r4 * (uint32_t)p.ldz + 8 * cg;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = r0 + 4 * rg + i;
-    dhv[i] = load(p.dh + row * p.lddh + col);
-    gv[i] = load(p.z + row * p.ldz + col);
-    uv[i] = load(p.z + row * p.ldz + p.n + col);
+    for (int i = 0; i < 4; ++i) {
+      const uint16_t *const dr = p.dh + (rw + i) * p.lddh + c0, *const zr = p.z + (rw + i) * p.ldz + c0;
+      dhv[i] = load(dr + od);
+      gv[i] = load(zr + oz);
+      uv[i] = load(zr + p.n + oz);
+    }
   }
   float x[3][4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     gated_slopes<ACT>(dhv[i], gv[i], uv[i], x[0][i], x[1][i], x[2][i]);
-    const int64_t row = r0 + 4 * rg + i;
     if (p.dz) {
-      *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = pack8(x[0][i]);
-      *reinterpret_cast<uint4*>(p.dz + row * p.lddz + p.n + col) = pack8(x[1][i]);
+      uint16_t* const zr = p.dz + (rw + i) * p.lddz + c0;
+      const uint32_t o = r4 * (uint32_t)p.lddz + 8 * cg;
+      store(zr + o, pack8(x[0][i]), 3);
+      store(zr + p.n + o, pack8(x[1][i]), 3);
     }
-    if (p.h) *reinterpret_cast<uint4*>(p.h + row * p.ldh + col) = pack8(x[2][i]);
+    if (p.h) store(p.h + (rw + i) * p.ldh + c0 + (r4 * (uint32_t)p.ldh + 8 * cg), pack8(x[2][i]), 3);
     if (p.q) {
-      uint8_t* const qr = p.q + row * p.ldq + col;
-      float* const sr = p.s + row * (2 * p.n / kGroup) + bx;
-      store_row_codes(x[0][i], x[1][i], qr, qr + p.n, sr, sr + p.n / kGroup, cg);
+      const RowCodes o = code_row(x[0][i], x[1][i]);
+      uint8_t* const qr = p.q + (rw + i) * p.ldq + c0;
+      const uint32_t oq = r4 * (uint32_t)p.ldq + 8 * cg;
+      *reinterpret_cast<uint2*>(qr + oq) = o.g;
+      *reinterpret_cast<uint2*>(qr + p.n + oq) = o.u;
+      if (cg == 0) {
+        const uint32_t lds = 2 * (uint32_t)p.n / kGroup;
+        float* const sr = p.s + (rw + i) * lds + bx;
+        sr[r4 * lds] = o.sg;
+        sr[r4 * lds + lds / 2] = o.su;
+      }
     }
     __builtin_amdgcn_sched_barrier(0);         // a row at a time: few live temporaries
   }
@@ -276,20 +311,33 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
     const int64_t ld = q == 2 ? p.ldqht : p.ldqt;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int c = 64 * i + (tid >> 3), k = tid & 7;
-      const uint4 v = *reinterpret_cast<const uint4*>(&codes[q][c * 32 + 4 * (k ^ ((c >> 3) & 7))]);
-      *reinterpret_cast<uint4*>(out + (c0 + c) * ld + r0 + 16 * k) = v;
+      const int cw = 64 * i + 8 * wave, cl = lane >> 3, k = lane & 7;
+      const uint4 v = *reinterpret_cast<const uint4*>(&codes[q][(cw + cl) * 32 + 4 * (k ^ wave)]);
+      store(out + (c0 + cw) * ld + r0 + (cl * (uint32_t)ld + 16 * k), v, 2);
     }
   }
 }
 
 template <int ACT>
 static int launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s) {
-  const bool stream = 6 * a.m * a.n > kStreamBytes;
+  const int64_t size = a.m * a.n;
+  // What passes through with the non-temporal hint, by degrees (kStreamBytes is half the last-level cache):
+  //   1  reads and writes exceed it: the inputs, and without transposed outputs dz and h
+  //   2  the writes alone do: the transposed codes too (the codes along the columns stay: the
+  //      activation gradient reads them next)
+  //   3  the writes exceed twice that, the whole cache: dz and h of the squares too
+  // Squares with codes alone, outputs in new memory / in one place: 8192 x 2048 53 / 49 us at degree 0, 47 / 47 at
+  // 1, 48 / 48 at 2; 16384 x 2048 85 / 76 at 1, 75 / 76 at 2; 8192 x 7168 144 / 125 and 117 / 117; 65536 x 1408
+  // 230 / 221 and 207 / 186; every store past the caches 87, 124 and 191.  4096 x 2048, 93 MB in all, 18.6 at 0 and
+  // 21.4 at 1.  With dz and h, 11008 x 2048 73 at 2 and 78 at 3, 8192 x 7168 220 and 180.
+  const int64_t writes = size * ((a.dz ? 4 : 0) + (a.q ? 2 : 0) + (a.qt ? 2 : 0) + (a.h ? 2 : 0) + (a.qht ? 1 : 0));
+  const int stream = 6 * size + writes <= kStreamBytes ? 0 : writes <= kStreamBytes ? 1 : writes <= 2 * kStreamBytes ? 2 : 3;
   if (a.qt || a.qht) {
     const dim3 grid((unsigned)((a.n / kGroup) * (a.m / kGroup)));
-    if (stream) hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, true>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, false>), grid, dim3(512), 0, s, a);
+    if (stream == 3) hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, 3>), grid, dim3(512), 0, s, a);
+    else if (stream == 2) hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, 2>), grid, dim3(512), 0, s, a);
+    else if (stream) hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, 1>), grid, dim3(512), 0, s, a);
+    else hipLaunchKernelGGL((gated_bwd_square_kernel<ACT, 0>), grid, dim3(512), 0, s, a);
     return launch_status();
   }
   const int64_t pieces_n = (a.n + kGroup - 1) / kGroup, pieces = a.m * pieces_n;
@@ -395,7 +443,10 @@ extern "C" int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint
   const bool cols = qt || qht;
   if (m < 0 || n <= 0 || n % 8 || n > 0x3FFFFFFFLL || m > 0x7FFFFFFFLL || ((q || cols) && n % kGroup) ||
       (cols && (m % kGroup || row_end || m / kGroup > 65535)) || m > kMaxGrid / ((n + kGroup - 1) / kGroup) - 16 || lddh < n ||
-      ldz < 2 * n || (dz && lddz < 2 * n) || (q && ldq < 2 * n) || (qt && ldqt < m) || (h && ldh < n) || (qht && ldqht < m))
+      ldz < 2 * n || (dz && lddz < 2 * n) || (q && ldq < 2 * n) || (qt && ldqt < m) || (h && ldh < n) || (qht && ldqht < m) ||
+      (cols && (lddh > kMaxSquareStride || ldz > kMaxSquareStride || (dz && lddz > kMaxSquareStride) ||
+                (q && ldq > kMaxSquareStride) || (qt && ldqt > kMaxSquareStride) || (h && ldh > kMaxSquareStride) ||
+                (qht && ldqht > kMaxSquareStride))))
     return FP8BS_ERR_SHAPE;
   if (!aligned(dh, 16) || lddh % 8 || !aligned(z, 16) || ldz % 8 || (dz && (!aligned(dz, 16) || lddz % 8)) ||
       (q && (!aligned(q, 16) || ldq % 16)) || (qt && (!aligned(qt, 16) || ldqt % 16)) || (h && (!aligned(h, 16) || ldh % 8)) ||

@@ -603,7 +603,7 @@ int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t t
  *            last expert segment, seg_offsets + num_experts)
  * Codes are the nearest to x / s of the unrounded FP32 values x (the quotient within two units in its last place).
  * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
- * m % 128 == 0 and row_end NULL, m < 2^23.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an
+ * m % 128 == 0 and row_end NULL, m < 2^23, strides < 2^28.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an
  * input, but dz may be z and h may be dh (same pointer and stride).
  * Alignment: bf16 and code pointers 16 bytes, bf16 strides % 8 == 0, code strides % 16 == 0, scales and row_end 4 bytes.
  */

@@ -107,6 +107,17 @@ def test_gated_backward_refusals(lib, change, status):
 def test_gated_backward_without_rows(lib):
     assert call(lib.raw.fp8bs_gated_backward, BWD, m=0) == OK
     assert call(lib.raw.fp8bs_gated_backward, BWD, **dict(NONE, m=0, dh=None, z=None)) == OK
+
+
+@pytest.mark.parametrize("stride", ["lddh", "ldz", "lddz", "ldq", "ldqt", "ldh", "ldqht"])
+def test_gated_backward_stride_limit_of_transposed_outputs(lib, stride):
+    assert call(lib.raw.fp8bs_gated_backward, BWD, **{stride: 1 << 28}) == ESHAPE
+    assert call(lib.raw.fp8bs_gated_backward, BWD, **{stride: (1 << 28) - 16, "m": 0}) == OK
+    without = dict(NONE, dz=P, q=P, s=P, h=P, m=0)
+    assert call(lib.raw.fp8bs_gated_backward, BWD, **{**without, stride: 1 << 28}) == OK
+    alone = dict(NONE, qt=P, st=P, m=0)          # strides of outputs that are left out do not count
+    assert call(lib.raw.fp8bs_gated_backward, BWD, **{**alone, stride: 1 << 28}) == \
+        (ESHAPE if stride in ("lddh", "ldz", "ldqt") else OK)
     assert call(lib.raw.fp8bs_gated_backward, BWD, m=0, act=9) == EFLAG
 
 

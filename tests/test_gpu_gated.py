@@ -297,6 +297,50 @@ def test_backward_both_orientations(gpu_lib, m, n, act):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+@pytest.mark.parametrize("wide", ["z", "dz", "qt"])
+def test_backward_of_the_largest_strides(gpu_lib, wide):
+    """Rows 2^28 elements apart, less the alignment: offsets within a square pass 2^31, of a matrix 2^32."""
+    m, n, stride = 128, 128, (1 << 28) - 16
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of free memory")
+    dh, z = backward_inputs(gen(28), m, n)
+    dh, z = dh.cuda(), z.cuda()
+    want = gpu_lib.fp8bs_gated_backward(dh, z, q=None, qt=None, h=None, qht=None)
+    rows, cols, dtype = (2 * n, m, torch.uint8) if wide == "qt" else (m, 2 * n, torch.bfloat16)
+    far = torch.empty(rows * stride, dtype=dtype, device="cuda").as_strided((rows, cols), (stride, 1))
+    out = dict(dz=None, q=None, qt=None, h=None, qht=None)
+    if wide == "z":
+        z = far.copy_(z)
+    elif wide == "dz":
+        out["dz"] = far
+    else:
+        out.update(qt=far, scales_t=torch.empty(2 * n, 1, device="cuda"))
+    got = gpu_lib.fp8bs_gated_backward(dh, z, **out)
+    for a, b in zip(got, want):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.view(torch.uint8))
+    del far, z, got, out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m,n,everything", [(8192, 2048, False), (16384, 2048, False), (16384, 2048, True)])
+def test_large_backward_has_the_bits_of_its_parts(gpu_lib, m, n, everything):
+    """Large calls pass through the caches in other ways (more than 128 MiB read and written, written, more than 256 MiB
+    written): the same bits as calls on 2048 rows each."""
+    g = gen(m)
+    dh = (torch.randn(m, n, generator=g) * 1e-3).bfloat16().cuda()
+    z = torch.randn(m, 2 * n, generator=g).bfloat16().cuda()
+    extra = dict(h=None) if everything else dict(dz=False)
+    whole = gpu_lib.fp8bs_gated_backward(dh, z, q=None, qt=None, qht=None, **extra)
+    for r in range(0, m, 2048):
+        part = gpu_lib.fp8bs_gated_backward(dh[r:r + 2048], z[r:r + 2048], q=None, qt=None, qht=None, **extra)
+        for i, (a, b) in enumerate(zip(whole, part)):
+            if b is None:
+                assert a is None
+                continue
+            a = a[:, r // 128:r // 128 + 16] if i in (4, 7) else a[:, r:r + 2048] if i in (3, 6) else a[r:r + 2048]
+            assert torch.equal(a.contiguous().view(torch.uint8), b.view(torch.uint8)), i
+
+
 def test_backward_tiny_and_zero_groups(gpu_lib):
     """Gradients whose groups have subnormal scales, and groups of zeros, in both orientations."""
     m, n = 256, 256
