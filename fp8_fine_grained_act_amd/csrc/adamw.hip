@@ -19,8 +19,8 @@
 // states in 8 bits.  32 lanes x 4 elements make a group, so FP32 arrays are read in whole
 // 16-byte pieces and a group's amax stays in registers.  One quad per lane and many
 // waves keep more of the memory busy than several quads per lane: eight 4096 x 7168
-// weights with states in 8 bits take 682 us (6.2 TB/s) on one, 729 on two, 784 on four (all with the
-// non-temporal hint; without it 5.4 TB/s), with FP32 states 1.19 ms (5.9 TB/s), 1.26, 1.31.  The table of tensors travels in
+// weights with states in 8 bits take 677 us (6.3 TB/s) on one, 729 on two, 784 on four (all with the
+// non-temporal hint; without it 5.4 TB/s), with FP32 states 1.18 ms (5.9 TB/s), 1.26, 1.31.  The table of tensors travels in
 // the kernel's arguments, kPerLaunch tensors each: no device copy of it, nothing to
 // keep alive under a captured graph.
 
@@ -95,17 +95,17 @@ struct AdamwStep {
 };
 
 // 4 consecutive elements per lane.  FULL: all inside the tensor; else elements from n on read as
-// zero and are not written.  STREAM: non-temporal accesses.
-template <bool FULL, bool STREAM>
+// zero and are not written.  STREAM: non-temporal accesses (1: but for bf16 parameters' stores).
+template <bool FULL, int STREAM>
 struct Quad {
   int64_t n;
   template <typename T>
   __device__ __forceinline__ T get(const void* p) const {
     return STREAM ? __builtin_nontemporal_load(static_cast<const T*>(p)) : *static_cast<const T*>(p);
   }
-  template <typename T>
+  template <typename T, int FROM = 1>
   __device__ __forceinline__ void put(void* p, T v) const {
-    if (STREAM) __builtin_nontemporal_store(v, static_cast<T*>(p));
+    if (STREAM >= FROM) __builtin_nontemporal_store(v, static_cast<T*>(p));
     else *static_cast<T*>(p) = v;
   }
   typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
@@ -149,7 +149,7 @@ struct Quad {
   __device__ __forceinline__ void store(uint16_t* dst, const float (&x)[4], int64_t i) const {
     const u32x2 w = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     if (FULL || i + 4 <= n) {
-      put<u32x2>(dst + i, w);
+      put<u32x2, 2>(dst + i, w);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -176,17 +176,14 @@ __device__ __forceinline__ uint2 state_codes(const float (&m)[4], const float (&
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     mq[j] = f32_quotient<SLOW>(m[j], mg);
-    // rounding upwards with the probability of q's place needs q cut off, not rounded: one unit less where
-    // its remainder is negative (-0.5 of the bits' 2^-20 on average otherwise, all upwards)
-    float q = fminf(f32_quotient<SLOW>(r[j], rg), kE4M3Max);
-    const float left = __builtin_fmaf(-q, rg.s * rg.up, r[j] * rg.up);
-    q = __int_as_float(__float_as_int(q) + (__float_as_int(left) >> 31));
+    // q is rounded to 2^-20 of a step, the random bits' unit, to nearest: no bias on average
+    const float q = fminf(f32_quotient<SLOW>(r[j], rg), kE4M3Max);
     rq[j] = fmaxf(round_at_random(q, mix32(random + (uint32_t)j * 0x9E3779B1u) >> 12), r[j] > 0.0f ? 0x1p-9f : 0.0f);
   }
   return make_uint2(code4_f32(mq[0], mq[1], mq[2], mq[3]), code4_f32(rq[0], rq[1], rq[2], rq[3]));
 }
 
-template <bool EIGHT, bool FULL, bool STREAM>
+template <bool EIGHT, bool FULL, int STREAM>
 __device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTensor& t, const AdamwStep& st, int64_t i) {
   const Quad<FULL, STREAM> io{t.n};
   float p[4], g[4], m[4], v[4], ms, rs;
@@ -239,7 +236,12 @@ __device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTenso
     return;
   }
   // elements past the end are zero here: their gradient and codes were read as zero
-  const F32Scale mg = f32_scale(max32_f32(mt)), rg = f32_scale(max32_f32(rt));
+  mt = max32_f32(mt);
+  rt = max32_f32(rt);
+  // amax times 1 / 448, within 1.5 units of the last place of the quotient: the codes are x / s with this s, and a
+  // chain of tensor operations that divides by a number multiplies by its reciprocal too, so that states
+  // stay the same over many steps (an s one unit off moves some codes, and those the next step's s)
+  const F32Scale mg = f32_scale_as(mt * (1.0f / kE4M3Max), mt), rg = f32_scale_as(rt * (1.0f / kE4M3Max), rt);
   const uint32_t random = st.key + (uint32_t)i * 0x9E3779B1u;
   const bool slow = __ballot(fmaxf(mg.up, rg.up) != 1.0f) != 0;
   const uint2 w = slow ? state_codes<true>(m, r, mg, rg, random) : state_codes<false>(m, r, mg, rg, random);
@@ -251,7 +253,7 @@ __device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTenso
   }
 }
 
-template <bool EIGHT, bool STREAM>
+template <bool EIGHT, int STREAM>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamwArgs a) {
   // the workgroup's tensor: the last whose first workgroup is not past this one
   int k = 0;
@@ -315,6 +317,12 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
   a.seed = seed;
   a.step = (uint32_t)step;
   a.scalars = scalars;
+  // Accesses pass the caches where a launch touches more than half the last-level cache.  New bf16 parameters stay in
+  // it, for the forward pass that reads them next, as long as all of the step's fit into that half: three 1536 x 7168
+  // (66 MB) with FP32 states 172 -> 164 us, in 8 bits 101 -> 97; eight 4096 x 7168 (470 MB) 677 -> 696, where they do not.
+  int64_t params = 0;
+  for (int64_t i = 0; i < num_tensors; ++i)
+    if (tensors[i].param_bf16) params += 2 * tensors[i].n;
   // launches of up to kPerLaunch tensors of one kind of state, in order
   int64_t i = 0;
   while (i < num_tensors) {
@@ -341,11 +349,15 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
     }
     const dim3 grid((unsigned)blocks), block(256);
     hipStream_t s = (hipStream_t)stream;
-    const bool large = bytes > kStreamBytes;
-    if (eight && large) hipLaunchKernelGGL((adamw_kernel<true, true>), grid, block, 0, s, a);
-    else if (eight) hipLaunchKernelGGL((adamw_kernel<true, false>), grid, block, 0, s, a);
-    else if (large) hipLaunchKernelGGL((adamw_kernel<false, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((adamw_kernel<false, false>), grid, block, 0, s, a);
+    const int stream = bytes <= kStreamBytes ? 0 : params <= kStreamBytes ? 1 : 2;
+    switch (3 * eight + stream) {
+      case 0: hipLaunchKernelGGL((adamw_kernel<false, 0>), grid, block, 0, s, a); break;
+      case 1: hipLaunchKernelGGL((adamw_kernel<false, 1>), grid, block, 0, s, a); break;
+      case 2: hipLaunchKernelGGL((adamw_kernel<false, 2>), grid, block, 0, s, a); break;
+      case 3: hipLaunchKernelGGL((adamw_kernel<true, 0>), grid, block, 0, s, a); break;
+      case 4: hipLaunchKernelGGL((adamw_kernel<true, 1>), grid, block, 0, s, a); break;
+      default: hipLaunchKernelGGL((adamw_kernel<true, 2>), grid, block, 0, s, a); break;
+    }
     const int st = launch_status();
     if (st != FP8BS_OK) return st;
   }

@@ -58,15 +58,16 @@ __device__ __forceinline__ float over_448(float amax) {
   return amax < 0x1p-100f ? amax / kE4M3Max : over_448_normal(amax);
 }
 constexpr float kTinyGroup = 0x1p-64f;         // below: the slow forms
-__device__ __forceinline__ F32Scale f32_scale(float amax) {
+__device__ __forceinline__ F32Scale f32_scale_as(float s, float amax) {   // s near amax / 448
   F32Scale g;
-  g.s = over_448(amax);
+  g.s = s;
   g.up = amax < kTinyGroup ? kTinyScale : 1.0f;
   const float d = g.s * g.up;
   g.r = d == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(d);
   g.rl = __builtin_fmaf(-d, g.r, 1.0f) * g.r;
   return g;
 }
+__device__ __forceinline__ F32Scale f32_scale(float amax) { return f32_scale_as(over_448(amax), amax); }
 // SLOW: some group of the wave is that small.
 template <bool SLOW>
 __device__ __forceinline__ float f32_quotient(float x, const F32Scale& g) {

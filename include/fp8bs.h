@@ -637,7 +637,7 @@ typedef struct fp8bs_adamw_tensor {
 /*
  * One step over tensors[0 .. num_tensors) (HOST memory, read before the call returns; types may differ from tensor to
  * tensor).  All arithmetic in FP32.  States in 8 bits: a scale per 128 consecutive elements (the last group may be
- * shorter), amax / 448; m rounds to nearest, sqrt(v) to one of its two neighbouring codes at random, upwards with the
+ * shorter), amax times 1 / 448; m rounds to nearest, sqrt(v) to one of its two neighbouring codes at random, upwards with the
  * probability that its distance from the lower one gives, and never from a positive value to zero.  The update of p
  * uses the new m and v before they are rounded.  The random bits are a function of (seed, step, the tensor's index in
  * the table, the element's index), so equal calls give equal bits.
