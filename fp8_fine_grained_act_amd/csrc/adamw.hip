@@ -5,15 +5,25 @@
 //
 // The states are FP32, or E4M3 codes in groups of 128 consecutive elements with one FP32
 // scale each (amax / 448, the library's tiles): m, and r = sqrt(v), whose range of
-// 2^18 in a group is 2^36 of v.  m is rounded to nearest: a step moves it by (1 - b1)(g -
-// m), far more than the codes' spacing.  r is rounded at random (upwards with the
+// 2^18 in a group is 2^36 of v.  r is rounded at random (upwards with the
 // probability that its place between two codes gives): one step moves v by at most 1 - b2
 // of itself downwards, less than half the codes' spacing, so rounding to nearest would
 // never let r fall.  r > 0 never becomes code 0, which bounds m / sqrt(v).  The update
 // of p uses the new m and v before they are rounded.
 //
+// m is rounded to nearest (half the error of a random rounding) where that lets it fall, and
+// at random elsewhere.  Without a gradient a step takes (1 - b1) |m|, and to nearest a code of
+// at most 0.5 / (1 - b1) units would stay as it is for ever while sqrt(v) falls: a weight without a gradient would
+// move on at up to some lr a step (0.15 lr on average with b1 0.9, hundreds with 0.95 and one live weight in the
+// group).  The subnormal codes have 0 to 7 units, all others 8 to 15, so
+//   (1 - b1) 8 < 0.5    any code could be held: m is rounded at random everywhere
+//   else                only subnormal ones: at random from a subnormal code to a subnormal code
+// but for states that are still zero as a whole.  Without a gradient m is then zero after some 40 / (1 - b1) steps.  An
+// ordinary code that is rounded to nearest may still rest up to 0.5 / (1 - b1) units beside a gradient that does not
+// change at all (5 units of 8 to 15 with b1 0.9).
+//
 // Random bits: 32-bit mixes of (seed, step), of the tensor's number, of the element's place; 20
-// of them stand for the fraction below an E4M3 step.
+// of them stand for the fraction below an E4M3 step of r, 20 of their mix for m's.
 //
 // Bound by HBM: 30 bytes per element with an FP32 master and FP32 states, 18.1 with
 // states in 8 bits.  32 lanes x 4 elements make a group, so FP32 arrays are read in whole
@@ -56,6 +66,7 @@ struct AdamwArgs {
   float lr, beta1, beta2, rest1, rest2, eps, grad_scale;   // rest = 1 - beta
   float unbias1, root2;                        // 1 / (1 - beta1^step), sqrt(1 / (1 - beta2^step))
   float log1, log2;                            // ln beta, for a step that is on the device
+  float held;                                  // m's codes below this could be held by rounding to nearest
   uint32_t seed, step;
   const float* scalars;                        // lr, grad_scale, step on the device, or null
 };
@@ -168,17 +179,27 @@ struct Quad {
   }
 };
 
-// codes of a group's m (to nearest) and r (at random)
+// Codes of a group's m (to nearest; at random where the old code `md` and the new one are below `held`) and r (at random).
 template <bool SLOW>
 __device__ __forceinline__ uint2 state_codes(const float (&m)[4], const float (&r)[4], const F32Scale& mg, const F32Scale& rg,
-                                             uint32_t random) {
+                                             const float (&md)[4], float held, uint32_t random) {
   float mq[4], rq[4];
+  uint32_t bits[4];
+  bool some = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    bits[j] = mix32(random + (uint32_t)j * 0x9E3779B1u);
     mq[j] = f32_quotient<SLOW>(m[j], mg);
+    some = some || (fabsf(md[j]) < held && fabsf(mq[j]) < held);
     // q is rounded to 2^-20 of a step, the random bits' unit, to nearest: no bias on average
     const float q = fminf(f32_quotient<SLOW>(r[j], rg), kE4M3Max);
-    rq[j] = fmaxf(round_at_random(q, mix32(random + (uint32_t)j * 0x9E3779B1u) >> 12), r[j] > 0.0f ? 0x1p-9f : 0.0f);
+    rq[j] = fmaxf(round_at_random(q, bits[j] >> 12), r[j] > 0.0f ? 0x1p-9f : 0.0f);
+  }
+  if (__ballot(some)) {                        // with b1 up to 0.9375 few waves hold such a value
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (fabsf(md[j]) < held && fabsf(mq[j]) < held)      // not a NaN
+        mq[j] = copysignf(round_at_random(fminf(fabsf(mq[j]), kE4M3Max), mix32(bits[j] + 0x3C6EF373u) >> 12), mq[j]);
   }
   return make_uint2(code4_f32(mq[0], mq[1], mq[2], mq[3]), code4_f32(rq[0], rq[1], rq[2], rq[3]));
 }
@@ -186,7 +207,7 @@ __device__ __forceinline__ uint2 state_codes(const float (&m)[4], const float (&
 template <bool EIGHT, bool FULL, int STREAM>
 __device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTensor& t, const AdamwStep& st, int64_t i) {
   const Quad<FULL, STREAM> io{t.n};
-  float p[4], g[4], m[4], v[4], ms, rs;
+  float p[4], g[4], m[4], v[4], md[4], ms, rs;
   uint32_t mc, rc;
   if (t.grad_bf16) io.load(g, static_cast<const uint16_t*>(t.grad), i);
   else io.load(g, static_cast<const float*>(t.grad), i);
@@ -206,9 +227,10 @@ __device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTenso
     typedef float v2f __attribute__((ext_vector_type(2)));
     const v2f m0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc, false), m1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc, true);
     const v2f r0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)rc, false), r1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)rc, true);
-    const float md[4] = {m0.x, m0.y, m1.x, m1.y}, rd[4] = {r0.x, r0.y, r1.x, r1.y};
+    const float mv[4] = {m0.x, m0.y, m1.x, m1.y}, rd[4] = {r0.x, r0.y, r1.x, r1.y};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      md[j] = mv[j];
       m[j] = md[j] * ms;
       const float r = rd[j] * rs;
       v[j] = r * r;
@@ -244,7 +266,8 @@ __device__ __forceinline__ void adamw_block(const AdamwArgs& a, const AdamwTenso
   const F32Scale mg = f32_scale_as(mt * (1.0f / kE4M3Max), mt), rg = f32_scale_as(rt * (1.0f / kE4M3Max), rt);
   const uint32_t random = st.key + (uint32_t)i * 0x9E3779B1u;
   const bool slow = __ballot(fmaxf(mg.up, rg.up) != 1.0f) != 0;
-  const uint2 w = slow ? state_codes<true>(m, r, mg, rg, random) : state_codes<false>(m, r, mg, rg, random);
+  const float held = ms > 0.0f ? a.held : 0.0f;     // states that are zero as a whole hold nothing
+  const uint2 w = slow ? state_codes<true>(m, r, mg, rg, md, held, random) : state_codes<false>(m, r, mg, rg, md, held, random);
   io.store_codes(t.avg, w.x, i);
   io.store_codes(t.sq, w.y, i);
   if ((threadIdx.x & 31) == 0 && (FULL || i < t.n)) {
@@ -310,6 +333,7 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
   a.grad_scale = (float)grad_scale;
   a.log1 = (float)log(beta1);
   a.log2 = (float)log(beta2);
+  a.held = (1.0 - beta1) * 8.0 < 0.5 ? INFINITY : 0x1p-6f;
   if (!scalars) {
     a.unbias1 = (float)(1.0 / (1.0 - pow(beta1, (double)step)));
     a.root2 = (float)sqrt(1.0 / (1.0 - pow(beta2, (double)step)));

@@ -637,9 +637,11 @@ typedef struct fp8bs_adamw_tensor {
 /*
  * One step over tensors[0 .. num_tensors) (HOST memory, read before the call returns; types may differ from tensor to
  * tensor).  All arithmetic in FP32.  States in 8 bits: a scale per 128 consecutive elements (the last group may be
- * shorter), amax times 1 / 448; m rounds to nearest, sqrt(v) to one of its two neighbouring codes at random, upwards with the
- * probability that its distance from the lower one gives, and never from a positive value to zero.  The update of p
- * uses the new m and v before they are rounded.  The random bits are a function of (seed, step, the tensor's index in
+ * shorter), amax times 1 / 448; sqrt(v) rounds to one of its two neighbouring codes at random, upwards with the
+ * probability that its distance from the lower one gives, and never from a positive value to zero.  m rounds to nearest,
+ * but at random (by its size, with bits of its own) where rounding to nearest could hold it without a gradient: from a
+ * subnormal code to a subnormal one, and for beta1 > 0.9375 everywhere; states whose scale is still 0 round to nearest.
+ * The update of p uses the new m and v before they are rounded.  The random bits are a function of (seed, step, the tensor's index in
  * the table, the element's index), so equal calls give equal bits.
  *   scalars  f32 [3] on the device: lr, grad_scale and step (a whole number from 1 to 2^24), read when the kernels run
  *            and in place of the arguments of these names (a step captured into a graph); or NULL
