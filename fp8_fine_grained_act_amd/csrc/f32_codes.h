@@ -6,7 +6,12 @@
 
 namespace fp8bs {
 
-// max of non-negative floats (they order as their bits) over aligned groups of 16
+// the larger magnitude of the two, a NaN if either is one (v_maximum3_f32; fmaxf would drop it)
+__device__ __forceinline__ float top_of(float a, float b) {
+  return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
+}
+
+// max of non-negative floats (they order as their bits, a NaN above all others) over aligned groups of 16
 // lanes, and with the lane 16 or 32 away (a swap of the operand with itself leaves
 // both lanes' values in each)
 __device__ __forceinline__ float max16_f32(float v) {
@@ -42,6 +47,7 @@ __device__ __forceinline__ float max_swap32_f32(float a, float b) {
 //   such an s carries fewer bits, so the quotient is clipped to 448 there (elsewhere it
 //   stays below 448 (1 + 2^-21), which codes as 448).  Where s underflows to zero
 //   (amax < 2^-141) the codes are signed zeros.
+//   An amax that is NaN (top_of) or infinite gives s = NaN and NaN codes: such a group is NaN as a whole.
 // F32Scale holds 1 / s as r + rl, to about 2^-46: x / s by f32_quotient, two operations
 // that round once more.  f32_quotient_fast takes x * r alone, within two units in the last
 // place: the code then differs from the exact quotient's only where that lies within
@@ -68,16 +74,20 @@ __device__ __forceinline__ F32Scale f32_scale_as(float s, float amax) {   // s n
   return g;
 }
 __device__ __forceinline__ F32Scale f32_scale(float amax) { return f32_scale_as(over_448(amax), amax); }
-// SLOW: some group of the wave is that small.
+// SLOW: some group of the wave may be that small.  Only such groups are clipped, which hold no NaN (v_med3_f32
+// would make it a number).
+__device__ __forceinline__ float clip_tiny(float q, float up) {
+  return up != 1.0f ? __builtin_amdgcn_fmed3f(q, -kE4M3Max, kE4M3Max) : q;
+}
 template <bool SLOW>
 __device__ __forceinline__ float f32_quotient(float x, const F32Scale& g) {
   if (!SLOW) return __builtin_fmaf(x, g.r, x * g.rl);
   const float v = x * g.up;
-  return __builtin_amdgcn_fmed3f(__builtin_fmaf(v, g.r, v * g.rl), -kE4M3Max, kE4M3Max);
+  return clip_tiny(__builtin_fmaf(v, g.r, v * g.rl), g.up);
 }
 template <bool SLOW>
 __device__ __forceinline__ float f32_quotient_fast(float x, float r, float up) {
-  return SLOW ? __builtin_amdgcn_fmed3f(x * up * r, -kE4M3Max, kE4M3Max) : x * r;
+  return SLOW ? clip_tiny(x * up * r, up) : x * r;
 }
 // The second conversion overwrites the first one's upper half, for which a stands (no register to clear).
 __device__ __forceinline__ uint32_t code4_f32(float a, float b, float c, float d) {

@@ -22,6 +22,13 @@
 
 namespace fp8bs {
 
+__device__ __forceinline__ float top8(const float (&x)[8]) {
+  float t = top_of(x[0], x[1]);
+#pragma unroll
+  for (int i = 2; i < 8; ++i) t = top_of(t, x[i]);
+  return t;
+}
+
 // ---- codes of h from its FP32 values -----------------------------------------------
 // h [m, n] FP32 contiguous -> 1x128 tiles along the columns.  16 lanes per tile, 8 values each.  With
 // seg only the rows of segments (between the first offset and the last).  A launch of its
@@ -38,10 +45,7 @@ __global__ __launch_bounds__(256) void quant_h_kernel(const float* __restrict__ 
   const float4* const src = reinterpret_cast<const float4*>(hf + row * n + tb * kGroup + 8 * lane16);
   const float4 a = src[0], b = src[1];
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-  const F32Scale g = f32_scale(max16_f32(top));
+  const F32Scale g = f32_scale(max16_f32(top8(x)));
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = f32_quotient<true>(x[i], g);
@@ -95,13 +99,6 @@ __device__ __forceinline__ void gated_slopes(uint4 dh, uint4 g, uint4 u, float (
     du[i] = d * a;
     h[i] = a * uv;
   }
-}
-
-__device__ __forceinline__ float top8(const float (&x)[8]) {
-  float t = fabsf(x[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) t = fmaxf(t, fabsf(x[i]));
-  return t;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
@@ -260,7 +257,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
     float t[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      t[j] = fmaxf(fmaxf(fabsf(x[q][0][j]), fabsf(x[q][1][j])), fmaxf(fabsf(x[q][2][j]), fabsf(x[q][3][j])));
+      t[j] = top_of(top_of(x[q][0][j], x[q][1][j]), top_of(x[q][2][j], x[q][3][j]));
     // over the wave's four groups of 16 lanes, two columns to a swap: afterwards group gr holds
     // columns 4 (gr % 2) + 2 (gr / 2) and the next of its 8
 #pragma unroll
@@ -274,7 +271,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
     const int q = tid >> 7, c = tid & 127;
     float t = tops[q][0][c];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) t = fmaxf(t, tops[q][w][c]);
+    for (int w = 1; w < 8; ++w) t = top_of(t, tops[q][w][c]);
     const F32Scale g = f32_scale(t);
     rcps[q][c] = g.r;
     ups[q][c] = g.up;

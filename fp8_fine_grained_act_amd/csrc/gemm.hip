@@ -1466,7 +1466,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       for (int j = 0; j < decltype(groups)::value; ++j) {
         float t = 0.0f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) t = fmaxf(t, fmaxf(fabsf(acc[0][j][v]), fabsf(acc[1][j][v])));
+        for (int v = 0; v < 4; ++v) t = top_of(t, top_of(acc[0][j][v], acc[1][j][v]));
         t = max_xor32_f32(max_xor16_f32(t));
         if (g == 0) tops[wn][ra0 + kGroupRows * j] = t;
       }
@@ -1476,7 +1476,7 @@ __global__ __launch_bounds__(64 * (MW + 4)) void gemm_ws_kernel(GemmArgs p) {
       for (int j = 0; j < decltype(groups)::value; ++j) {
         const int r = ra0 + kGroupRows * j;
         const int64_t row = m0 + r;
-        const F32Scale sc = f32_scale(fmaxf(fmaxf(tops[0][r], tops[1][r]), fmaxf(tops[2][r], tops[3][r])));
+        const F32Scale sc = f32_scale(top_of(top_of(tops[0][r], tops[1][r]), top_of(tops[2][r], tops[3][r])));
         uint32_t code[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -559,7 +559,8 @@ int fp8bs_grouped_wgrad_ragged(const uint16_t* dy, int64_t ldy, const uint16_t* 
  *   h   bf16 [m, n], row stride ldh, or NULL: h rounded once
  *   qh, sh  E4M3 [m, n], row stride ldqh bytes, and f32 [m, n/128], or both NULL: the 1x128
  *       tiles of the unrounded h along the columns, the down projection's input (s =
- *       amax / 448, codes to nearest even of h / s)
+ *       amax / 448, codes to nearest even of h / s; a tile with a NaN or an infinity has scale NaN, so that
+ *       every value it stands for is NaN)
  *   workspace  16-byte aligned, at least fp8bs_gemm_gated_workspace(m, n, k) bytes, used only by
  *       this call until it has run (two captured graphs that may run at once need one
  *       each); may be NULL where that is 0 or qh is NULL
@@ -601,7 +602,8 @@ int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t t
  *   qht, scales_ht E4M3 [n, m], row stride ldqht, f32 [n, m/128]: the same of h (weight gradients: fp8bs_gemm_wgrad)
  *   row_end  int32 on the device, or NULL: rows from *row_end on are neither read nor written (the end of the
  *            last expert segment, seg_offsets + num_experts)
- * Codes are the nearest to x / s of the unrounded FP32 values x (the quotient within two units in its last place).
+ * Codes are the nearest to x / s of the unrounded FP32 values x (the quotient within two units in its last place); a tile
+ * with a NaN or an infinity has scale NaN.
  * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
  * m % 128 == 0 and row_end NULL, m < 2^23, strides < 2^28.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an
  * input, but dz may be z and h may be dh (same pointer and stride).
