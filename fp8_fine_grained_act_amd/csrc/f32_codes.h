@@ -49,9 +49,9 @@ __device__ __forceinline__ float max_swap32_f32(float a, float b) {
 //   (amax < 2^-141) the codes are signed zeros.
 //   An amax that is NaN (top_of) or infinite gives s = NaN and NaN codes: such a group is NaN as a whole.
 // F32Scale holds 1 / s as r + rl, to about 2^-46: x / s by f32_quotient, two operations
-// that round once more.  f32_quotient_fast takes x * r alone, within two units in the last
-// place: the code then differs from the exact quotient's only where that lies within
-// 2^-22 of a midpoint between two codes, 2^-18 of a code's own rounding.
+// that round once more: the binary32 quotient, but where the exact one lies within 2^-46 of a
+// boundary between two of them.  (x * r alone is within two units in the last place; a few codes in 10^5 are
+// then not the nearest.)
 struct F32Scale {
   float s, r, rl, up;
 };
@@ -74,6 +74,10 @@ __device__ __forceinline__ F32Scale f32_scale_as(float s, float amax) {   // s n
   return g;
 }
 __device__ __forceinline__ F32Scale f32_scale(float amax) { return f32_scale_as(over_448(amax), amax); }
+__device__ __forceinline__ F32Scale f32_scale_ordinary(float amax) {     // not below kTinyGroup
+  const float s = over_448_normal(amax), r = __builtin_amdgcn_rcpf(s);
+  return F32Scale{s, r, __builtin_fmaf(-s, r, 1.0f) * r, 1.0f};
+}
 // SLOW: some group of the wave may be that small.  Only such groups are clipped, which hold no NaN (v_med3_f32
 // would make it a number).
 __device__ __forceinline__ float clip_tiny(float q, float up) {
@@ -84,10 +88,6 @@ __device__ __forceinline__ float f32_quotient(float x, const F32Scale& g) {
   if (!SLOW) return __builtin_fmaf(x, g.r, x * g.rl);
   const float v = x * g.up;
   return clip_tiny(__builtin_fmaf(v, g.r, v * g.rl), g.up);
-}
-template <bool SLOW>
-__device__ __forceinline__ float f32_quotient_fast(float x, float r, float up) {
-  return SLOW ? clip_tiny(x * up * r, up) : x * r;
 }
 // The second conversion overwrites the first one's upper half, for which a stands (no register to clear).
 __device__ __forceinline__ uint32_t code4_f32(float a, float b, float c, float d) {

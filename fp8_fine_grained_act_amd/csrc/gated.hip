@@ -106,31 +106,26 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 // 8 codes of one row's tile piece of dg and of du, their scales stored by the tiles' first lane (16 lanes a
-// tile).  Where every group of the wave is of ordinary size, a scale takes three operations and its reciprocal one.
+// tile).  Where every group of the wave is of ordinary size, a scale takes three operations and its reciprocal three.
 template <bool SLOW>
-__device__ __forceinline__ uint2 row_codes(const float (&x)[8], float r, float up) {
+__device__ __forceinline__ uint2 row_codes(const float (&x)[8], const F32Scale& g) {
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = f32_quotient_fast<SLOW>(x[i], r, up);
+  for (int i = 0; i < 8; ++i) v[i] = f32_quotient<SLOW>(x[i], g);
   return make_uint2(code4_f32(v[0], v[1], v[2], v[3]), code4_f32(v[4], v[5], v[6], v[7]));
 }
 struct RowCodes {
   uint2 g, u;                // codes of dg and du
   float sg, su;
 };
+template <bool SLOW>
+__device__ __forceinline__ RowCodes code_row_by(const float (&dg)[8], const float (&du)[8], const F32Scale& g, const F32Scale& u) {
+  return RowCodes{row_codes<SLOW>(dg, g), row_codes<SLOW>(du, u), g.s, u.s};
+}
 __device__ __forceinline__ RowCodes code_row(const float (&dg)[8], const float (&du)[8]) {
   const float a = max16_f32(top8(dg)), b = max16_f32(top8(du));
-  RowCodes o;
-  if (__ballot(fminf(a, b) < kTinyGroup)) {
-    const F32Scale ga = f32_scale(a), gb = f32_scale(b);
-    o = RowCodes{row_codes<true>(dg, ga.r, ga.up), row_codes<true>(du, gb.r, gb.up), ga.s, gb.s};
-  } else {
-    o.sg = over_448_normal(a);
-    o.su = over_448_normal(b);
-    o.g = row_codes<false>(dg, __builtin_amdgcn_rcpf(o.sg), 1.0f);
-    o.u = row_codes<false>(du, __builtin_amdgcn_rcpf(o.su), 1.0f);
-  }
-  return o;
+  if (__ballot(fminf(a, b) < kTinyGroup)) return code_row_by<true>(dg, du, f32_scale(a), f32_scale(b));
+  return code_row_by<false>(dg, du, f32_scale_ordinary(a), f32_scale_ordinary(b));
 }
 
 // Without transposed outputs: 16 lanes per piece of 128 columns of a row.
@@ -197,7 +192,8 @@ constexpr int64_t kMaxSquareStride = (1 << 28) - 1;
 template <int ACT, int STREAM>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_square_kernel(GatedBwdArgs p) {
   __shared__ float tops[3][8][128];            // [dg, du, h][wave][column]
-  __shared__ float rcps[3][128], ups[3][128];  // a column's r and up
+  __shared__ float2 rcps[3][128];              // a column's r and rl
+  __shared__ float ups[3][128];                // and its up
   __shared__ int tiny;                         // some up is not 1
   __shared__ __attribute__((aligned(16))) uint32_t codes[3][128 * 32];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -273,7 +269,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
 #pragma unroll
     for (int w = 1; w < 8; ++w) t = top_of(t, tops[q][w][c]);
     const F32Scale g = f32_scale(t);
-    rcps[q][c] = g.r;
+    rcps[q][c] = make_float2(g.r, g.rl);
     ups[q][c] = g.up;
     if (g.up != 1.0f) tiny = 1;
     if (q >= q0 && q < nq) {
@@ -289,10 +285,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
       if (q < q0 || q >= nq) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float r = rcps[q][8 * cg + j], up = SLOW ? ups[q][8 * cg + j] : 1.0f;
+        const float2 r = rcps[q][8 * cg + j];
+        const F32Scale col{0.0f, r.x, r.y, SLOW ? ups[q][8 * cg + j] : 1.0f};
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = f32_quotient_fast<SLOW>(x[q][i][j], r, up);
+        for (int i = 0; i < 4; ++i) v[i] = f32_quotient<SLOW>(x[q][i][j], col);
         codes[q][(8 * cg + j) * 32 + (rg ^ ((cg & 7) << 2))] = code4_f32(v[0], v[1], v[2], v[3]);
         __builtin_amdgcn_sched_barrier(0);     // a column at a time: few live scales
       }

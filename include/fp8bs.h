@@ -602,8 +602,7 @@ int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t t
  *   qht, scales_ht E4M3 [n, m], row stride ldqht, f32 [n, m/128]: the same of h (weight gradients: fp8bs_gemm_wgrad)
  *   row_end  int32 on the device, or NULL: rows from *row_end on are neither read nor written (the end of the
  *            last expert segment, seg_offsets + num_experts)
- * Codes are the nearest to x / s of the unrounded FP32 values x (the quotient within two units in its last place); a tile
- * with a NaN or an infinity has scale NaN.
+ * Codes are the nearest to x / s of the unrounded FP32 values x; a tile with a NaN or an infinity has scale NaN.
  * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
  * m % 128 == 0 and row_end NULL, m < 2^23, strides < 2^28.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an
  * input, but dz may be z and h may be dh (same pointer and stride).
