@@ -30,8 +30,26 @@ __device__ __forceinline__ float top8(const float (&x)[8]) {
 }
 
 // ---- codes of h from its FP32 values -----------------------------------------------
+// Whether some segment holds row first + i, bit i for i < 16, for the whole workgroup of 256 threads: an expert per
+// thread and step.  Offsets outside the rows need no clipping, a segment that runs backwards holds none.
+__device__ __forceinline__ uint32_t rows_of_segments(const int32_t* __restrict__ seg, int64_t num_experts, int64_t first) {
+  __shared__ uint32_t held;
+  if (threadIdx.x == 0) held = 0;
+  __syncthreads();
+  uint32_t mine = 0;
+  for (int64_t e = threadIdx.x; e < num_experts; e += 256) {
+    const int64_t lo = max((int64_t)seg[e] - first, (int64_t)0), hi = min((int64_t)seg[e + 1] - first, (int64_t)16);
+    if (lo < hi) mine |= (1u << hi) - (1u << lo);
+  }
+  if (mine) atomicOr(&held, mine);
+  __syncthreads();
+  return held;
+}
+
 // h [m, n] FP32 contiguous -> 1x128 tiles along the columns.  16 lanes per tile, 8 values each.  With
-// seg only the rows of segments (between the first offset and the last).  A launch of its
+// seg only the rows of segments.  Every row from the first offset to the last is one: offsets lead from the one to
+// the other and pass it upwards somewhere.  The others are looked for in all segments (rows behind the last one are
+// in none, but where offsets run backwards they may be).  A launch of its
 // own, 2 us for a few rows, 8 us (4.7 TB/s) for 4096 x 2048.
 __global__ __launch_bounds__(256) void quant_h_kernel(const float* __restrict__ hf, int64_t m, int64_t n,
                                                       const int32_t* __restrict__ seg, int64_t num_experts,
@@ -40,8 +58,14 @@ __global__ __launch_bounds__(256) void quant_h_kernel(const float* __restrict__ 
   const uint32_t tiles_n = (uint32_t)(n / kGroup);
   const uint32_t t = blockIdx.x * 16u + (threadIdx.x >> 4);
   const int64_t row = t / tiles_n, tb = t - (uint32_t)row * tiles_n;
+  if (seg) {
+    const int64_t first = blockIdx.x * 16u / tiles_n, last = (blockIdx.x * 16u + 15u) / tiles_n;   // at most 16 rows
+    if (first < seg[0] || last >= seg[num_experts]) {      // the same for the whole workgroup
+      const uint32_t held = rows_of_segments(seg, num_experts, first);
+      if (!(held >> (row - first) & 1)) return;
+    }
+  }
   if (row >= m) return;                        // the 16 lanes of a tile together
-  if (seg && (row < seg[0] || row >= seg[num_experts])) return;
   const float4* const src = reinterpret_cast<const float4*>(hf + row * n + tb * kGroup + 8 * lane16);
   const float4 a = src[0], b = src[1];
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};

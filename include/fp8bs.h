@@ -490,7 +490,9 @@ int64_t fp8bs_epilogue_backward_workspace(int64_t m, int64_t n);
  * non-decreasing within [0, total_rows]; offsets outside are clipped and a
  * segment that runs backwards counts as empty, so no contents lead to an access
  * outside the buffers.  Rows that belong to no segment are neither read nor
- * written.
+ * written.  (Offsets that run backwards can put a row into several segments: it
+ * gets the result of one of them, and if all segments together have more than
+ * total_rows rows, some rows may keep what they held.)
  */
 
 /*
