@@ -460,7 +460,7 @@ extern "C" int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint
   if (act < FP8BS_ACT_NONE || act > FP8BS_ACT_SILU) return FP8BS_ERR_FLAG;
   const bool cols = qt || qht;
   if (m < 0 || n <= 0 || n % 8 || n > 0x3FFFFFFFLL || m > 0x7FFFFFFFLL || ((q || cols) && n % kGroup) ||
-      (cols && (m % kGroup || row_end || m / kGroup > 65535)) || m > kMaxGrid / ((n + kGroup - 1) / kGroup) - 16 || lddh < n ||
+      (cols && (m % kGroup || row_end || m / kGroup > 65535)) || m > (kMaxGrid - 16) / ((n + kGroup - 1) / kGroup) || lddh < n ||
       ldz < 2 * n || (dz && lddz < 2 * n) || (q && ldq < 2 * n) || (qt && ldqt < m) || (h && ldh < n) || (qht && ldqht < m) ||
       (cols && (lddh > kMaxSquareStride || ldz > kMaxSquareStride || (dz && lddz > kMaxSquareStride) ||
                 (q && ldq > kMaxSquareStride) || (qt && ldqt > kMaxSquareStride) || (h && ldh > kMaxSquareStride) ||

@@ -605,9 +605,9 @@ int64_t fp8bs_grouped_gemm_gated_ragged_workspace(int64_t num_experts, int64_t t
  *   row_end  int32 on the device, or NULL: rows from *row_end on are neither read nor written (the end of the
  *            last expert segment, seg_offsets + num_experts)
  * Codes are the nearest to x / s of the unrounded FP32 values x; a tile with a NaN or an infinity has scale NaN.
- * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0; n % 128 == 0 for codes; for qt or qht also
- * m % 128 == 0 and row_end NULL, m < 2^23, strides < 2^28.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap each other or an
- * input, but dz may be z and h may be dh (same pointer and stride).
+ * m >= 0 (0: nothing is done, no pointer is needed), n % 8 == 0, n < 2^30; n % 128 == 0 for codes; for qt or qht also
+ * m % 128 == 0 and row_end NULL, m < 2^23, strides < 2^28.  m ceil(n / 128) < 2^31 - 16.  The outputs must not overlap
+ * each other or an input, but dz may be z and h may be dh (same pointer and stride).
  * Alignment: bf16 and code pointers 16 bytes, bf16 strides % 8 == 0, code strides % 16 == 0, scales and row_end 4 bytes.
  */
 int fp8bs_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* z, int64_t ldz, int64_t m, int64_t n, int act,
