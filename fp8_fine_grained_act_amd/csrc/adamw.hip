@@ -309,7 +309,9 @@ extern "C" int fp8bs_adamw_step(const fp8bs_adamw_tensor* tensors, int64_t num_t
                                 double eps, int64_t step, double grad_scale, const float* scalars, uint32_t seed, void* stream) {
   if (num_tensors < 0 || num_tensors > 0x7FFFFFFFLL) return FP8BS_ERR_SHAPE;
   if (num_tensors > 0 && !tensors) return FP8BS_ERR_NULL;
-  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || (!scalars && step < 1))
+  // below 2^-126 the reciprocal of eps overflows: a weight that never had a gradient would become 0 times infinity
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps == 0.0 || eps >= 0x1p-126) ||
+      (!scalars && step < 1))
     return FP8BS_ERR_FLAG;
   if (!aligned(scalars, 4)) return FP8BS_ERR_ALIGN;
   for (int64_t i = 0; i < num_tensors; ++i) {

@@ -648,7 +648,9 @@ typedef struct fp8bs_adamw_tensor {
  * the table, the element's index), so equal calls give equal bits.
  *   scalars  f32 [3] on the device: lr, grad_scale and step (a whole number from 1 to 2^24), read when the kernels run
  *            and in place of the arguments of these names (a step captured into a graph); or NULL
- * No tensor may overlap another, but gradients may be shared.  Gradients and their squares must be finite in FP32.  0 <= beta < 1, eps >= 0, step >= 1 (else FP8BS_ERR_FLAG).  Never allocates.
+ * No tensor may overlap another, but gradients may be shared.  Gradients and their squares must be finite in FP32.
+ * 0 <= beta < 1, eps 0 (a weight that never had a gradient is then 0 / 0) or at least 2^-126, step >= 1 (else
+ * FP8BS_ERR_FLAG).  Never allocates.
  * Alignment: param, master, grad, avg, sq 16 bytes, scales and scalars 4 bytes.  FP8BS_ERR_NULL also when exactly one
  * of avg_scales, root_scales is NULL; FP8BS_ERR_FLAG for a master beside an f32 param.  Everything is checked before
  * the first kernel is enqueued.
