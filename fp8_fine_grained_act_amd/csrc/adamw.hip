@@ -29,7 +29,7 @@
 // states in 8 bits.  32 lanes x 4 elements make a group, so FP32 arrays are read in whole
 // 16-byte pieces and a group's amax stays in registers.  One quad per lane and many
 // waves keep more of the memory busy than several quads per lane: eight 4096 x 7168
-// weights with states in 8 bits take 677 us (6.3 TB/s) on one, 729 on two, 784 on four (all with the
+// weights with states in 8 bits take 677-688 us (6.2 TB/s) on one, 729 on two, 784 on four (all with the
 // non-temporal hint; without it 5.4 TB/s), with FP32 states 1.18 ms (5.9 TB/s), 1.26, 1.31.  The table of tensors travels in
 // the kernel's arguments, kPerLaunch tensors each: no device copy of it, nothing to
 // keep alive under a captured graph.

@@ -9,8 +9,8 @@
 // rows, transposed (weight gradients of both weights; h's for the down projection).
 // Bound by HBM: 6 bytes read per element of h, 2 to 10 written.  Without transposed outputs
 // 32768 x 2048 in 140 us with dz, h and codes (6.7 TB/s), 16384 x 2048 with codes alone in 43
-// us (6.3 TB/s); with both orientations and h's, 16384 x 2048 in 76-78 us (4.9 TB/s), where the
-// arithmetic (34 VALU instructions per element, 34 us of issue) and the phases between
+// us (6.2 TB/s); with both orientations and h's, 16384 x 2048 in 78-82 us (4.7 TB/s), where the
+// arithmetic (38 VALU instructions per element, 37 us of issue) and the phases between
 // barriers of only two squares per CU come on top.
 
 #include <type_traits>
@@ -347,7 +347,8 @@ static int launch_gated_bwd(const GatedBwdArgs& a, hipStream_t s) {
   // Squares with codes alone, outputs in new memory / in one place: 8192 x 2048 53 / 49 us at degree 0, 47 / 47 at
   // 1, 48 / 48 at 2; 16384 x 2048 85 / 76 at 1, 75 / 76 at 2; 8192 x 7168 144 / 125 and 117 / 117; 65536 x 1408
   // 230 / 221 and 207 / 186; every store past the caches 87, 124 and 191.  4096 x 2048, 93 MB in all, 18.6 at 0 and
-  // 21.4 at 1.  With dz and h, 11008 x 2048 73 at 2 and 78 at 3, 8192 x 7168 220 and 180.
+  // 21.4 at 1.  With dz and h, 11008 x 2048 73 at 2 and 78 at 3, 8192 x 7168 220 and 180.  (Measured with the codes
+  // from one product with the reciprocal; they take up to 6 us more now, at any degree.)
   const int64_t writes = size * ((a.dz ? 4 : 0) + (a.q ? 2 : 0) + (a.qt ? 2 : 0) + (a.h ? 2 : 0) + (a.qht ? 1 : 0));
   const int stream = 6 * size + writes <= kStreamBytes ? 0 : writes <= kStreamBytes ? 1 : writes <= 2 * kStreamBytes ? 2 : 3;
   if (a.qt || a.qht) {
