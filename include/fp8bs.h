@@ -40,7 +40,8 @@
  *     multiplier, not rounded to a power of two).  Code of x: E4M3
  *     round-to-nearest-even of the binary32 quotient x / s, saturating at
  *     +-448, sign kept also for zeros.  A group with amax == 0 gets s = 0 and
- *     signed-zero codes.  No flush-to-zero anywhere.
+ *     signed-zero codes.  No flush-to-zero anywhere.  (The optimizer's 8-bit
+ *     states take amax times 1 / 448, see fp8bs_adamw_step.)
  *   - Every 128-element scale group lies along the contraction of the GEMM
  *     that consumes it, so each 128-long partial is multiplied by one
  *     activation scale and one weight scale and added into an FP32
